@@ -60,7 +60,8 @@ typedef enum {
     RA_ERR_INVALID = 1,      /* bad argument: null/misaligned pointer, bad size or divisibility */
     RA_ERR_UNSUPPORTED = 2,  /* valid request the library does not implement (e.g. D not in {32,64,128}) */
     RA_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed; see ra_last_error() */
-    RA_ERR_TIMEOUT = 4       /* a kernel gave up on a bounded internal wait; outputs are undefined */
+    RA_ERR_TIMEOUT = 4,      /* a kernel gave up on a bounded internal wait; outputs are undefined */
+    RA_ERR_INDEX = 5         /* a cache kernel met a page, length or token count outside its bounds */
 } ra_status;
 
 typedef enum {
@@ -419,10 +420,126 @@ RA_API ra_status ra_ulysses_head2seq_grouped(const void* in, void* out, int P, i
                                              int Lc, int H, int D, ra_dtype dt, void* stream);
 
 /*
+ * ---- Attention over a K/V cache: what serving a model trained with the calls above needs.
+ * Conventions of ra_paged_kv_append and ra_prefix_attn_fwd:
+ *   - Cache: k_pages, v_pages, bf16, n_pages pages of [page_size][H_kv][D], page i starting
+ *     i*page_stride elements in (page_stride >= page_size*H_kv*D, so K and V pages may be
+ *     interleaved in one allocation).  Any page_size >= 1.
+ *   - Batch: B sequences with n_b >= 0 new tokens each, ragged: the tokens of sequence b are
+ *     rows cu_tokens[b] .. cu_tokens[b+1]-1 of q, k, v and out (cu_tokens: device int32,
+ *     [B+1], not decreasing, starting at >= 0).  Rows at or past cu_tokens[B] (a padded
+ *     batch) are neither read nor written.  n_tokens: rows of the token tensors, the host's
+ *     bound on cu_tokens[B]; max_tokens: the host's bound on every n_b.
+ *   - seq_lens: device int32, [B]: keys of sequence b's own in the cache, its new tokens
+ *     included (they are the last n_b of them).
+ *   - block_tables: device int32, [B][max_pages]: key j of sequence b is row j % page_size of
+ *     page block_tables[b][j / page_size].  Entries past a sequence's length are not read.
+ *   - The device arrays may change between launches of a captured graph; host arguments are
+ *     bounds and stay.
+ *   - Device values outside their bounds (n_b > max_tokens, seq_lens[b] > max_len or < n_b
+ *     for the append, a page id outside [0, n_pages)) are never followed: the kernel skips
+ *     or clamps them, what it writes for that sequence is undefined, and ra_sync_status()
+ *     returns RA_ERR_INDEX.
+ */
+
+/*
+ * ra_paged_kv_append -- the new tokens' K and V into the paged cache, with the rotation of
+ * their positions (rotary embedding) applied to q and k on the way.
+ * Token i of sequence b's n_b sits at p = seq_lens[b] - n_b + i of its own keys and at
+ * sequence position pos_offset + p.  For j < rot_dim/2, with (x, y) the elements
+ * (j, j + rot_dim/2) of a head, or (2j, 2j + 1) with interleaved = 1:
+ *   angle = (pos_offset + p) * inv_freq[j]   (exact product; reduced in 64 bits)
+ *   (x, y) <- (x cos - y sin, y cos + x sin)   in fp32, rounded once to bf16
+ * Elements from rot_dim on, and all of v, are copied bit for bit.
+ *   q, q_out   device bf16, rows of [H_q][D], q_tstride / q_out_tstride elements apart;
+ *              q_out may be q itself (same stride).  H_q = 0: no queries (both null).
+ *   k, v       device bf16, rows of [H_kv][D], k_tstride / v_tstride elements apart.
+ *   inv_freq   device fp32, [rot_dim/2] (null where rot_dim is 0).
+ *   rot_dim    0 <= rot_dim <= D, a multiple of 16.
+ *   k_pages, v_pages  the cache (written).  Two tokens never share a row unless two tables
+ *              name the same page; which of them is kept is then unspecified.
+ * Errors: RA_ERR_INVALID for null or misaligned (16-byte; tables 4-byte) pointers, sizes
+ *   < 1, H_q < 0, H_q % H_kv != 0, strides below the dense size or not a multiple of 8
+ *   elements, rot_dim out of range, pos_offset < 0, interleaved not in {0,1};
+ *   RA_ERR_UNSUPPORTED for dtype other than RA_BF16 or D outside {64, 128}.
+ */
+RA_API ra_status ra_paged_kv_append(const void* q, const void* k, const void* v,
+                                    long long q_tstride, long long k_tstride,
+                                    long long v_tstride, const int* cu_tokens,
+                                    const int* seq_lens, const int* block_tables,
+                                    const float* inv_freq, int B, int n_tokens, int max_tokens,
+                                    int H_q, int H_kv, int D, int rot_dim, int interleaved,
+                                    int pos_offset, int page_size, int n_pages, int max_pages,
+                                    long long page_stride, ra_dtype dtype, void* q_out,
+                                    long long q_out_tstride, void* k_pages, void* v_pages,
+                                    void* stream);
+
+/*
+ * ra_prefix_attn_fwd -- attention of the new tokens over the paged cache, for a batch whose
+ * sequences share a prefix (a system prompt, a document) kept once in the cache.
+ * Token i of sequence b's n_b sees the prefix_len keys of the prefix and its own keys
+ * 0 .. seq_lens[b] - n_b + i; out and lse are ra_ring_attn_fwd's formulas over those keys.
+ * The prefix's keys are read once for the rows of the whole batch, each sequence's own keys
+ * once for its rows; the parts are joined by the log-sum-exp merge of ra_lse_merge.
+ * prefix_len = 0 is plain paged attention (one token per sequence: decode).  A row that sees
+ * no key gets out = 0, lse = -inf.  Keys and values that no row may see (past seq_lens[b],
+ * past prefix_len) may hold anything, NaN included; a key that a later token of the same
+ * sequence sees must be finite.
+ *   q             device bf16, rows of [H_q][D], q_tstride elements apart (already rotated).
+ *   prefix_table  device int32: key j of the prefix is row j % page_size of page
+ *                 prefix_table[j / page_size]; ceil(prefix_len / page_size) entries (null
+ *                 where prefix_len is 0).
+ *   max_len       the host's bound on seq_lens, 1 <= max_len <= max_pages * page_size.
+ *   out           device, out_dtype, dense [n_tokens][H_q][D].
+ *   lse           device fp32, dense [H_q][n_tokens], natural log.
+ *   workspace     device, 16-byte aligned, at least ra_prefix_attn_workspace(...) bytes
+ *                 (null where that is 0); its contents on return are unspecified.  Calls
+ *                 that may overlap in time need workspaces of their own.
+ * Reproducible: the same bits on every call with the same sizes and inputs.
+ * Errors: RA_ERR_INVALID as ra_paged_kv_append, for scale not finite and > 0, prefix_len < 0,
+ *   a workspace that is too small; RA_ERR_UNSUPPORTED for in_dtype other than RA_BF16 or D
+ *   outside {64, 128}.
+ */
+RA_API long long ra_prefix_attn_workspace(int B, int n_tokens, int max_tokens, int max_len,
+                                          int prefix_len, int H_q, int H_kv, int D,
+                                          int page_size);
+RA_API ra_status ra_prefix_attn_fwd(const void* q, long long q_tstride, const void* k_pages,
+                                    const void* v_pages, const int* cu_tokens,
+                                    const int* seq_lens, const int* block_tables,
+                                    const int* prefix_table, int prefix_len, int B, int n_tokens,
+                                    int max_tokens, int max_len, int H_q, int H_kv, int D,
+                                    int page_size, int n_pages, int max_pages,
+                                    long long page_stride, float scale, ra_dtype in_dtype,
+                                    ra_dtype out_dtype, void* out, float* lse, void* workspace,
+                                    long long workspace_bytes, void* stream);
+
+/*
+ * ra_cross_attn_fwd -- attention of Lq queries to the Lk states of an encoder (another
+ * length, no causal order), per batch row the first kv_lens[b] of them (padded batches).
+ * out and lse: ra_ring_attn_fwd's formulas over the keys j < kv_lens[b].  kv_lens[b] = 0:
+ * out = 0, lse = -inf.  States past kv_lens[b] may hold anything, NaN included.
+ *   q        device bf16, [B][Lq] rows of [H_q][D], q_tstride elements between tokens,
+ *            q_bstride between batch rows.
+ *   k, v     device bf16, [B][Lk] rows of [H_kv][D], kv_tstride and kv_bstride both.
+ *   kv_lens  device int32, [B] (clamped to [0, Lk]; above Lk is RA_ERR_INDEX at
+ *            ra_sync_status), or null: Lk everywhere.
+ *   out      device, out_dtype, dense [B][Lq][H_q][D];  lse  device fp32, dense [B][H_q][Lq].
+ *   workspace  at least ra_cross_attn_workspace(...) bytes, as for ra_prefix_attn_fwd.
+ * Errors: as ra_prefix_attn_fwd.
+ */
+RA_API long long ra_cross_attn_workspace(int B, int Lq, int Lk, int H_q, int H_kv, int D);
+RA_API ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v,
+                                   const int* kv_lens, int B, int Lq, int Lk, int H_q, int H_kv,
+                                   int D, long long q_tstride, long long q_bstride,
+                                   long long kv_tstride, long long kv_bstride, float scale,
+                                   ra_dtype in_dtype, ra_dtype out_dtype, void* out, float* lse,
+                                   void* workspace, long long workspace_bytes, void* stream);
+
+/*
  * ra_sync_status -- synchronise `stream`, then read and clear this device's
  * kernel error word.  Returns RA_ERR_TIMEOUT if a kernel launched since the
- * last call gave up on a bounded wait, RA_ERR_CUDA if the synchronisation
- * itself failed, RA_OK otherwise.
+ * last call gave up on a bounded wait, RA_ERR_INDEX if one met an index outside
+ * its bounds, RA_ERR_CUDA if the synchronisation itself failed, RA_OK otherwise.
  */
 RA_API ra_status ra_sync_status(void* stream);
 

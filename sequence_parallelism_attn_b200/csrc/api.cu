@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <string>
 #include "ra_internal.h"
+#include "kv_internal.h"
 #include "../../include/ra.h"
 
 namespace {
@@ -375,6 +376,9 @@ ra_status ra_sync_status(void* stream) {
     e = ra::read_and_clear_error_word(&word);
     if (e == cudaSuccess) e = ra::read_and_clear_permute_error(&pword);
     if (e == cudaSuccess) e = ra::read_and_clear_bwd_error(&bword);
+    unsigned int kword = 0, aword = 0;
+    if (e == cudaSuccess) e = ra::read_and_clear_kv_error(&kword);
+    if (e == cudaSuccess) e = ra::read_and_clear_append_error(&aword);
     if (e != cudaSuccess) return cuda_fail(e, "reading the kernel error word");
     word |= (pword ? 16u : 0u) | (bword ? 64u : 0u);
     if (word) {
@@ -383,6 +387,14 @@ ra_status ra_sync_status(void* stream) {
                       "a kernel gave up on a bounded wait (error bits 0x%x: 1 load, 2 mma, "
                       "4 softmax, 8 drain, 16 permute, 64 backward)", word);
         return fail(RA_ERR_TIMEOUT, buf);
+    }
+    kword |= aword;
+    if (kword) {
+        char buf[160];
+        std::snprintf(buf, sizeof buf,
+                      "a cache kernel met a value outside its bounds (bits 0x%x: 1 tokens of a "
+                      "sequence, 2 a length, 4 a page id)", kword);
+        return fail(RA_ERR_INDEX, buf);
     }
     return RA_OK;
 }

@@ -1,0 +1,66 @@
+// kv_internal.h -- what the operators over a K/V cache share: attention of new tokens over
+// a paged cache (with a prefix that the whole batch sees) or over an encoder's states, and
+// the append that fills the cache.  Arguments are validated by api_kv.cu.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+#include "ra_internal.h"
+
+namespace ra {
+
+constexpr int kSms = 148;  // a B200's SMs: the work split is planned for them, not queried
+
+// Bits of the device's cache error word (read and cleared by ra_sync_status).
+constexpr unsigned kKvErrTokens = 1u, kKvErrLength = 2u, kKvErrPage = 4u;
+
+struct AppendArgs {
+    const void *q, *k, *v;
+    long long q_tstride, k_tstride, v_tstride, q_out_tstride;  // elements between tokens
+    const int *cu, *lens, *tables;
+    const float* inv_freq;
+    int B, n_tokens, max_tokens, H_q, H_kv, D, rot, interleaved, pos_offset;
+    int page_size, n_pages, max_pages;
+    long long page_stride;  // elements
+    void *q_out, *k_pages, *v_pages;
+    cudaStream_t stream;
+};
+cudaError_t launch_paged_append(const AppendArgs& a);
+cudaError_t read_and_clear_append_error(unsigned int* value);
+
+// Queries and keys of one call.  Tokens of sequence b: cu[b] .. cu[b+1]-1 (ragged, cu given)
+// or Lq tokens of batch row b (cu null).  Keys of sequence b: its own lens[b] keys (all
+// max_len where lens is null) found through its page table (tables given) or in its dense
+// batch row (tables null: page b, of page_stride elements), and before them the prefix.
+struct KvArgs {
+    const void* q;
+    long long q_tstride, q_bstride;  // elements; q_bstride only where cu is null
+    const void *k, *v;
+    long long kv_tstride, page_stride;  // elements between tokens, between pages (batch rows)
+    const int *cu, *lens, *tables, *prefix_table;
+    int prefix_len, B, n_tokens, max_tokens, max_len;
+    int H_q, H_kv, D;
+    int page_size, n_pages, max_pages;
+    int causal;  // own keys: new token i of n sees keys up to len - n + i
+    float scale;
+    int out_bf16;
+    void* out;
+    float* lse;
+    void* workspace;
+    cudaStream_t stream;
+};
+
+// How a call is split: partial results of row (token, head) for every key range, joined by
+// the combine kernel.
+struct KvPlan {
+    int chunk_p, splits_p, tiles_p;  // prefix: keys per split, splits, row tiles
+    int chunk_o, splits_o, tiles_o;  // each sequence's own keys
+    int mt;                          // 16-row tiles per block
+    int direct;                      // one split in all: results written without partials
+    long long blocks, workspace;     // grid size, bytes
+};
+KvPlan plan_kv_rows(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
+                    int H_kv, int D);
+cudaError_t launch_kv_rows(const KvArgs& a, const KvPlan& p);
+cudaError_t read_and_clear_kv_error(unsigned int* value);
+
+}  // namespace ra

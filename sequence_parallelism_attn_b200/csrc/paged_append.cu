@@ -1,0 +1,173 @@
+// paged_append.cu -- K and V of new tokens into a paged cache, with the position rotation
+// applied to q and k on the way.
+//
+// Token i of sequence b (of its n_b new tokens, the last n_b of its length len_b) sits at
+// p = len_b - n_b + i of the sequence's own keys and at sequence position pos_offset + p.
+// With angle_j = (pos_offset + p) * inv_freq_j, the pair (x, y) of a head's elements
+// (j, j + R/2), or (2j, 2j+1) interleaved, becomes (x cos - y sin, y cos + x sin); elements
+// from R on are copied.  The product is formed and reduced to turns in 64 bits (one multiply
+// and one subtraction): a 32-bit product loses 2^-24 of an angle of up to millions of
+// radians.  The fraction that is left, at most half a turn, is exact enough in 32 bits
+// (relative 2^-24) for sincospif.
+#include <cuda_bf16.h>
+#include "kv_internal.h"
+
+namespace ra {
+
+__device__ unsigned int g_append_error_word = 0;
+
+namespace {
+
+constexpr int kTokens = 4;  // tokens per block
+
+struct AppendParams {
+    AppendArgs a;
+    int tiles;  // blocks per sequence
+};
+
+__device__ __forceinline__ void rotate2(uint32_t& xy_lo, uint32_t& xy_hi, float2 cs0, float2 cs1) {
+    // elements (lo of xy_lo with lo of xy_hi) by cs0, (hi with hi) by cs1
+    const float x0 = __uint_as_float(xy_lo << 16), x1 = __uint_as_float(xy_lo & 0xffff0000u);
+    const float y0 = __uint_as_float(xy_hi << 16), y1 = __uint_as_float(xy_hi & 0xffff0000u);
+    const __nv_bfloat162 a =
+        __floats2bfloat162_rn(x0 * cs0.x - y0 * cs0.y, x1 * cs1.x - y1 * cs1.y);
+    const __nv_bfloat162 b =
+        __floats2bfloat162_rn(y0 * cs0.x + x0 * cs0.y, y1 * cs1.x + x1 * cs1.y);
+    xy_lo = *reinterpret_cast<const uint32_t*>(&a);
+    xy_hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint32_t rotate1(uint32_t xy, float2 cs) {
+    const float x = __uint_as_float(xy << 16), y = __uint_as_float(xy & 0xffff0000u);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x * cs.x - y * cs.y, y * cs.x + x * cs.y);
+    return *reinterpret_cast<const uint32_t*>(&a);
+}
+
+// One thread moves two 16-byte vectors of one head: the two halves of 8 rotated pairs, or
+// neighbours.  Units of a token: (H_q + 2 H_kv) heads x D/16.
+template <int D>
+__global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int UPH = D / 16;
+    const AppendArgs& a = p.a;
+    __shared__ float2 cs[kTokens][D / 2];
+    __shared__ long long row_off[kTokens];  // element offset of the token's row in the cache
+    const int b = blockIdx.x / p.tiles, t0 = (blockIdx.x % p.tiles) * kTokens;
+    int c0 = a.cu[b], c1 = a.cu[b + 1];
+    const int len = max(a.lens[b], 0);
+    c0 = max(c0, 0);
+    c1 = min(c1, a.n_tokens);
+    const int n = c1 - c0;
+    if (threadIdx.x == 0 && t0 == 0 && n > a.max_tokens) atomicOr(&g_append_error_word, kKvErrTokens);
+    const int nt = min(n - t0, kTokens);
+    if (nt <= 0) return;
+    if (threadIdx.x < nt) {
+        const int pos = len - n + t0 + (int)threadIdx.x;
+        long long off = -1;
+        if (pos >= 0) {
+            const int slot = pos / a.page_size;
+            if (slot >= a.max_pages) {
+                atomicOr(&g_append_error_word, kKvErrLength);
+            } else {
+                const int page = a.tables[(long long)b * a.max_pages + slot];
+                if (page < 0 || page >= a.n_pages)
+                    atomicOr(&g_append_error_word, kKvErrPage);
+                else
+                    off = (long long)page * a.page_stride +
+                          (long long)(pos - slot * a.page_size) * a.H_kv * D;
+            }
+        } else {
+            atomicOr(&g_append_error_word, kKvErrLength);
+        }
+        row_off[threadIdx.x] = off;
+    }
+    const int half = a.rot / 2;
+    for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
+        const int t = i / half, j = i - t * half;
+        const double pos = (double)a.pos_offset + (double)(len - n + t0 + t);
+        double turns = pos * (double)a.inv_freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
+        turns -= rint(turns);
+        float s, c;
+        sincospif((float)(2.0 * turns), &s, &c);
+        cs[t][j] = make_float2(c, s);
+    }
+    __syncthreads();
+    const int units = (a.H_q + 2 * a.H_kv) * UPH;
+    const int ru = a.rot / 16;
+    for (int u = threadIdx.x; u < units; u += blockDim.x) {
+        const int head = u / UPH, j = u % UPH;
+        const bool is_q = head < a.H_q, is_v = head >= a.H_q + a.H_kv;
+        const int h = is_q ? head : (is_v ? head - a.H_q - a.H_kv : head - a.H_q);
+        const uint16_t* src = (const uint16_t*)(is_q ? a.q : (is_v ? a.v : a.k));
+        const long long stride = is_q ? a.q_tstride : (is_v ? a.v_tstride : a.k_tstride);
+        const bool turned = !is_v && j < ru;
+        int v0 = 2 * j, v1 = 2 * j + 1;  // the two vectors of the head
+        if (!a.interleaved && j < ru) {
+            v0 = j;
+            v1 = j + ru;
+        }
+        uint4 x[kTokens], y[kTokens];
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t)
+            if (t < nt) {
+                const uint4* r =
+                    reinterpret_cast<const uint4*>(src + (long long)(c0 + t0 + t) * stride + h * D);
+                x[t] = r[v0];
+                y[t] = r[v1];
+            }
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t)
+            if (t < nt) {
+                if (turned) {
+                    uint32_t* xs = reinterpret_cast<uint32_t*>(&x[t]);
+                    uint32_t* ys = reinterpret_cast<uint32_t*>(&y[t]);
+                    if (a.interleaved) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            xs[e] = rotate1(xs[e], cs[t][8 * j + e]);
+                            ys[e] = rotate1(ys[e], cs[t][8 * j + 4 + e]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            rotate2(xs[e], ys[e], cs[t][8 * j + 2 * e], cs[t][8 * j + 2 * e + 1]);
+                    }
+                }
+                uint4* w = nullptr;
+                if (is_q)
+                    w = reinterpret_cast<uint4*>((uint16_t*)a.q_out +
+                                                 (long long)(c0 + t0 + t) * a.q_out_tstride + h * D);
+                else if (row_off[t] >= 0)
+                    w = reinterpret_cast<uint4*>((uint16_t*)(is_v ? a.v_pages : a.k_pages) +
+                                                 row_off[t] + h * D);
+                if (w) {
+                    w[v0] = x[t];
+                    w[v1] = y[t];
+                }
+            }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const AppendArgs& a) {
+    AppendParams p;
+    p.a = a;
+    p.tiles = (a.max_tokens + kTokens - 1) / kTokens;
+    const int units = (a.H_q + 2 * a.H_kv) * (a.D / 16);
+    const int threads = units >= 384 ? 384 : ((units + 31) / 32) * 32;
+    const unsigned grid = (unsigned)((long long)p.tiles * a.B);
+    if (a.D == 128) append_kernel<128><<<grid, threads, 0, a.stream>>>(p);
+    else append_kernel<64><<<grid, threads, 0, a.stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t read_and_clear_append_error(unsigned int* value) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_append_error_word, sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    if (*value) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_append_error_word, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
+}  // namespace ra

@@ -16,6 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libra_b200.so")
 
 RA_OK, RA_ERR_INVALID, RA_ERR_UNSUPPORTED, RA_ERR_CUDA, RA_ERR_TIMEOUT = 0, 1, 2, 3, 4
+RA_ERR_INDEX = 5
 RA_BF16, RA_FP32 = 0, 1
 RA_MAX_P = 64
 EXPORTED = ("ra_ring_attn_fwd", "ra_ring_attn_fwd_zigzag", "ra_ring_attn_fwd_packed",
@@ -24,7 +25,9 @@ EXPORTED = ("ra_ring_attn_fwd", "ra_ring_attn_fwd_zigzag", "ra_ring_attn_fwd_pac
             "ra_lse_merge", "ra_ulysses_seq2head", "ra_ulysses_head2seq",
             "ra_ulysses_seq2head_grouped", "ra_ulysses_head2seq_grouped",
             "ra_ulysses_seq2head_scatter", "ra_ulysses_head2seq_scatter",
-            "ra_ulysses_replica_sum", "ra_sync_status", "ra_last_error", "ra_set_wait_limit_ns",
+            "ra_ulysses_replica_sum", "ra_paged_kv_append", "ra_prefix_attn_fwd",
+            "ra_prefix_attn_workspace", "ra_cross_attn_fwd", "ra_cross_attn_workspace",
+            "ra_sync_status", "ra_last_error", "ra_set_wait_limit_ns",
             "ra_set_bwd_deterministic", "ra_debug_inject_stall", "ra_version")
 
 
@@ -67,13 +70,24 @@ def load() -> ctypes.CDLL:
     lib.ra_ulysses_replica_sum.argtypes = [vp, vp, i64, i32, i32, i32, vp]
     lib.ra_ulysses_seq2head_scatter.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp]
     lib.ra_ulysses_head2seq_scatter.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp]
+    lib.ra_paged_kv_append.argtypes = ([vp] * 3 + [i64] * 3 + [vp] * 4 + [i32] * 12 +
+                                       [i64, i32, vp, i64, vp, vp, vp])
+    lib.ra_prefix_attn_fwd.argtypes = ([vp, i64] + [vp] * 6 + [i32] * 11 +
+                                       [i64, f32, i32, i32, vp, vp, vp, i64, vp])
+    lib.ra_cross_attn_fwd.argtypes = ([vp] * 4 + [i32] * 6 + [i64] * 4 +
+                                      [f32, i32, i32, vp, vp, vp, i64, vp])
+    lib.ra_prefix_attn_workspace.argtypes = [i32] * 9
+    lib.ra_cross_attn_workspace.argtypes = [i32] * 6
+    for f in ("ra_prefix_attn_workspace", "ra_cross_attn_workspace"):
+        getattr(lib, f).restype = i64
     lib.ra_sync_status.argtypes = [vp]
     for f in ("ra_ring_attn_fwd", "ra_ring_attn_fwd_zigzag", "ra_ring_attn_fwd_packed",
               "ra_ring_attn_bwd", "ra_ring_attn_bwd_zigzag", "ra_ring_attn_bwd_packed",
               "ra_ring_attn_bwd_static", "ra_ring_attn_bwd_accumulate", "ra_lse_merge",
               "ra_ulysses_seq2head", "ra_ulysses_head2seq", "ra_ulysses_seq2head_grouped",
               "ra_ulysses_head2seq_grouped", "ra_ulysses_replica_sum", "ra_sync_status",
-              "ra_ulysses_seq2head_scatter", "ra_ulysses_head2seq_scatter"):
+              "ra_ulysses_seq2head_scatter", "ra_ulysses_head2seq_scatter",
+              "ra_paged_kv_append", "ra_prefix_attn_fwd", "ra_cross_attn_fwd"):
         getattr(lib, f).restype = ctypes.c_int
     lib.ra_last_error.restype = ctypes.c_char_p
     lib.ra_version.restype = ctypes.c_char_p
@@ -417,4 +431,243 @@ def ring_attn_fwd(q: torch.Tensor, k_chunks, v_chunks, causal: bool, scale: floa
           P, B, H_q, H_kv, Lc, D, q.stride(0) if B > 1 else L * H_q * D,
           kv_bstride if B > 1 else Lc * H_kv * D, float(scale), int(bool(causal)),
           _dt(q.dtype), _dt(out.dtype), out.data_ptr(), lse.data_ptr(), _stream(stream))
+    return out, lse
+
+
+# ------------------------------------------------------------------ attention over a K/V cache
+def _where(t: torch.Tensor, stream):
+    """Context in which a call on t's device allocates and launches: t's device where it is
+    not the current one, and the stream that was given (so that what is allocated here
+    belongs to the stream that uses it)."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
+                                               device=t.device)
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return None
+
+
+def _rows(t: torch.Tensor, name: str, device) -> None:
+    """A tensor of token rows [..., H, D] whose heads are dense."""
+    H, D = t.shape[-2:]
+    if t.device != device or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bf16 tensor on {device}")
+    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+
+
+def _ints(t: torch.Tensor, name: str, device, shape) -> None:
+    if t.device != device or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+def _dense(t: torch.Tensor, name: str, device, shape, dtype) -> None:
+    if t.device != device or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+
+
+def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, device):
+    """(n_pages, page_size, H_kv, D, page stride) of a cache [n_pages, page_size, H_kv, D]."""
+    if k_pages.shape != v_pages.shape or k_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages must both be [n_pages, page_size, H_kv, D]")
+    n_pages, page_size, H_kv, D = k_pages.shape
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _rows(t, name, device)
+        if page_size > 1 and t.stride(1) != H_kv * D:
+            raise ValueError(f"{name}: the rows of a page must be dense")
+    stride = k_pages.stride(0) if n_pages > 1 else page_size * H_kv * D
+    if n_pages > 1 and v_pages.stride(0) != stride:
+        raise ValueError("k_pages and v_pages must have the same page stride")
+    return n_pages, page_size, H_kv, D, stride
+
+
+def _tstride(t: torch.Tensor, dim: int) -> int:
+    """Elements between tokens; the dense value where there is a single one."""
+    return t.stride(dim) if t.shape[dim] > 1 else t.shape[-2] * t.shape[-1]
+
+
+def paged_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                    k_pages: torch.Tensor, v_pages: torch.Tensor, cu_tokens: torch.Tensor,
+                    seq_lens: torch.Tensor, block_tables: torch.Tensor,
+                    inv_freq: torch.Tensor | None, max_tokens: int, pos_offset: int = 0,
+                    interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None):
+    """The new tokens' K and V into the paged cache, q and k rotated to their positions
+    (ra_paged_kv_append): q [N, H_q, D] or None, k and v [N, H_kv, D] (bf16; the tokens may
+    be strided, as slices of one projection are), k_pages / v_pages [n_pages, page_size,
+    H_kv, D], cu_tokens int32 [B + 1], seq_lens int32 [B] (the new tokens included),
+    block_tables int32 [B, max_pages], inv_freq fp32 [rot_dim / 2] (None: no rotation).
+    Returns the rotated q [N, H_q, D] (q_out, which may be q itself), or None without q."""
+    ctx = _where(k, stream)
+    if ctx is not None:
+        with ctx:
+            return paged_kv_append(q, k, v, k_pages, v_pages, cu_tokens, seq_lens, block_tables,
+                                   inv_freq, max_tokens, pos_offset, interleaved, q_out)
+    dev = k.device
+    n_pages, page_size, H_kv, D, page_stride = _cache(k_pages, v_pages, dev)
+    N = k.shape[0]
+    if tuple(k.shape) != (N, H_kv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [N, H_kv, D] with the cache's heads")
+    _rows(k, "k", dev)
+    _rows(v, "v", dev)
+    B, max_pages = block_tables.shape
+    _ints(cu_tokens, "cu_tokens", dev, (B + 1,))
+    _ints(seq_lens, "seq_lens", dev, (B,))
+    _ints(block_tables, "block_tables", dev, (B, max_pages))
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _dense(inv_freq, "inv_freq", dev, (rot // 2,), torch.float32)
+    H_q = q_ptr = q_ts = qo_ptr = qo_ts = 0
+    if q is not None:
+        H_q = q.shape[1]
+        if tuple(q.shape) != (N, H_q, D):
+            raise ValueError("q must be [N, H_q, D]")
+        _rows(q, "q", dev)
+        if q_out is None:
+            q_out = torch.empty((N, H_q, D), dtype=torch.bfloat16, device=dev)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        else:
+            _rows(q_out, "q_out", dev)
+        q_ptr, q_ts, qo_ptr, qo_ts = (q.data_ptr(), _tstride(q, 0), q_out.data_ptr(),
+                                      _tstride(q_out, 0))
+    _check(load().ra_paged_kv_append(
+        q_ptr, k.data_ptr(), v.data_ptr(), q_ts, _tstride(k, 0), _tstride(v, 0),
+        cu_tokens.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(),
+        inv_freq.data_ptr() if rot else None, B, N, min(max_tokens, N), H_q, H_kv, D, rot,
+        int(interleaved), pos_offset, page_size, n_pages, max_pages, page_stride, RA_BF16, qo_ptr,
+        qo_ts, k_pages.data_ptr(), v_pages.data_ptr(), _stream(None)))
+    return q_out if q is not None else None
+
+
+def _workspace(need: int, workspace: torch.Tensor | None, dev):
+    """(pointer, bytes) of the caller's workspace, or of a new one, and the tensor itself."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def prefix_attn_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                    cu_tokens: torch.Tensor, seq_lens: torch.Tensor, block_tables: torch.Tensor,
+                    max_tokens: int, max_len: int | None = None,
+                    prefix_table: torch.Tensor | None = None, prefix_len: int = 0,
+                    scale: float | None = None, out_dtype: torch.dtype = torch.float32,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Attention of the new tokens q [N, H_q, D] (bf16, rotated) over the paged cache
+    (ra_prefix_attn_fwd): the prefix_len keys of prefix_table's pages, which the whole batch
+    shares, then each sequence's own keys up to the token itself.  cu_tokens, seq_lens and
+    block_tables as for paged_kv_append; max_tokens and max_len bound them (max_len: the
+    tables' capacity by default; a closer bound splits the work better).  prefix_len = 0:
+    plain paged attention.  Rows past cu_tokens[B] are not written.  Returns
+    (out [N, H_q, D] in out_dtype, lse [H_q, N] fp32); the workspace
+    (ra_prefix_attn_workspace bytes) is allocated here when not given."""
+    ctx = _where(q, stream)
+    if ctx is not None:
+        with ctx:
+            return prefix_attn_fwd(q, k_pages, v_pages, cu_tokens, seq_lens, block_tables,
+                                   max_tokens, max_len, prefix_table, prefix_len, scale,
+                                   out_dtype, out, lse, workspace)
+    dev = q.device
+    n_pages, page_size, H_kv, D, page_stride = _cache(k_pages, v_pages, dev)
+    N, H_q, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q and the cache must have the same head dimension")
+    _rows(q, "q", dev)
+    B, max_pages = block_tables.shape
+    _ints(cu_tokens, "cu_tokens", dev, (B + 1,))
+    _ints(seq_lens, "seq_lens", dev, (B,))
+    _ints(block_tables, "block_tables", dev, (B, max_pages))
+    table = None
+    if prefix_len > 0:
+        if prefix_table is None or prefix_table.numel() * page_size < prefix_len:
+            raise ValueError("prefix_table must name ceil(prefix_len / page_size) pages")
+        _ints(prefix_table, "prefix_table", dev, (prefix_table.numel(),))
+        table = prefix_table.data_ptr()
+    if max_len is None:
+        max_len = max_pages * page_size
+    max_tokens = min(max_tokens, N)
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty((N, H_q, D), dtype=out_dtype, device=dev)
+    else:
+        _dense(out, "out", dev, (N, H_q, D), out.dtype)
+    if lse is None:
+        lse = torch.empty((H_q, N), dtype=torch.float32, device=dev)
+    else:
+        _dense(lse, "lse", dev, (H_q, N), torch.float32)
+    lib = load()
+    ws, ws_bytes, keep = _workspace(
+        lib.ra_prefix_attn_workspace(B, N, max_tokens, max_len, prefix_len, H_q, H_kv, D,
+                                     page_size), workspace, dev)
+    _check(lib.ra_prefix_attn_fwd(
+        q.data_ptr(), _tstride(q, 0), k_pages.data_ptr(), v_pages.data_ptr(),
+        cu_tokens.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(), table, prefix_len, B,
+        N, max_tokens, max_len, H_q, H_kv, D, page_size, n_pages, max_pages, page_stride, scale,
+        RA_BF16, _dt(out.dtype), out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _stream(None)))
+    return out, lse
+
+
+def _cross_strides(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
+    """Checked sizes and strides of cross attention's inputs."""
+    dev = q.device
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("q must be [B, Lq, H_q, D], k and v [B, Lk, H_kv, D]")
+    B, Lq, H_q, D = q.shape
+    _, Lk, H_kv, _ = k.shape
+    if k.shape[0] != B or k.shape[3] != D:
+        raise ValueError("q, k and v must have the same batch and head dimension")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _rows(t, name, dev)
+    qt, kt = _tstride(q, 1), _tstride(k, 1)
+    qb = q.stride(0) if B > 1 else max(Lq * qt, Lq * H_q * D)
+    kb = k.stride(0) if B > 1 else max(Lk * kt, Lk * H_kv * D)
+    if (Lk > 1 and v.stride(1) != kt) or (B > 1 and v.stride(0) != kb):
+        raise ValueError("k and v must have the same strides")
+    return B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb
+
+
+def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   kv_lens: torch.Tensor | None = None, scale: float | None = None,
+                   out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream=None):
+    """Attention of q [B, Lq, H_q, D] to an encoder's states k, v [B, Lk, H_kv, D] (bf16;
+    tokens and batch rows may be strided, k and v alike), per batch row the first kv_lens[b]
+    of them (int32 [B]; None: all) (ra_cross_attn_fwd).  Returns (out [B, Lq, H_q, D] in
+    out_dtype, lse [B, H_q, Lq] fp32)."""
+    ctx = _where(q, stream)
+    if ctx is not None:
+        with ctx:
+            return cross_attn_fwd(q, k, v, kv_lens, scale, out_dtype, out, lse, workspace)
+    dev = q.device
+    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v)
+    if kv_lens is not None:
+        _ints(kv_lens, "kv_lens", dev, (B,))
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty((B, Lq, H_q, D), dtype=out_dtype, device=dev)
+    else:
+        _dense(out, "out", dev, (B, Lq, H_q, D), out.dtype)
+    if lse is None:
+        lse = torch.empty((B, H_q, Lq), dtype=torch.float32, device=dev)
+    else:
+        _dense(lse, "lse", dev, (B, H_q, Lq), torch.float32)
+    lib = load()
+    ws, ws_bytes, keep = _workspace(lib.ra_cross_attn_workspace(B, Lq, Lk, H_q, H_kv, D),
+                                    workspace, dev)
+    _check(lib.ra_cross_attn_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if kv_lens is None else kv_lens.data_ptr(),
+        B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb, scale, RA_BF16, _dt(out.dtype), out.data_ptr(),
+        lse.data_ptr(), ws, ws_bytes, _stream(None)))
     return out, lse

@@ -1,0 +1,405 @@
+"""The operators over a K/V cache on the GPU against plain 64-bit forms: the paged append
+with its rotation, attention over the cache behind a shared prefix, the single-token and
+short forms of cross attention, and a run of them together."""
+import pytest
+import torch
+
+import _kv_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+NAN = float("nan")
+
+
+def randn(*shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).bfloat16()
+
+
+def i32(x):
+    return torch.as_tensor(x, dtype=torch.int32)
+
+
+class Batch:
+    """A ragged batch over a paged cache on the CPU: new tokens n[b], own lengths lens[b]."""
+
+    def __init__(self, n, lens, page, hkv, d, plen=0, seed=0, extra_rows=0, spare_pages=3,
+                 fill=NAN):
+        self.n, self.page = list(n), page
+        self.cu = i32([sum(n[:i]) for i in range(len(n) + 1)])
+        self.N = int(self.cu[-1]) + extra_rows
+        self.lens = i32(lens)
+        self.max_pages = max(1, -(-max(list(lens) + [1]) // page))
+        n_pre = -(-plen // page)
+        used = n_pre + sum(-(-x // page) for x in lens)
+        self.n_pages = used + spare_pages
+        ids = torch.randperm(self.n_pages, generator=torch.Generator().manual_seed(seed)).tolist()
+        self.ptable = i32([ids.pop() for _ in range(n_pre)])
+        # entries past a length are not read: an id far outside the cache stands there
+        self.tables = torch.full((len(n), self.max_pages), 1 << 29, dtype=torch.int32)
+        for b, x in enumerate(lens):
+            for j in range(-(-x // page)):
+                self.tables[b, j] = ids.pop()
+        # rows that hold no key are `fill`
+        self.kp = torch.full((self.n_pages, page, hkv, d), fill).bfloat16()
+        self.vp = self.kp.clone()
+        k, v = randn(used * page, hkv, d, seed=seed + 1), randn(used * page, hkv, d, seed=seed + 2)
+        at = 0
+        for table, x in [(self.ptable, plen)] + [(self.tables[b], x) for b, x in enumerate(lens)]:
+            for j in range(x):
+                self.kp[int(table[j // page]), j % page] = k[at]
+                self.vp[int(table[j // page]), j % page] = v[at]
+                at += 1
+        self.plen = plen
+
+    def gpu(self, *names):
+        return [getattr(self, n).to(DEV) for n in names]
+
+
+PREFIX = [  # n, lens, page, hq, hkv, d, prefix
+    ([1], [1], 16, 4, 2, 64, 0),
+    ([1], [17], 16, 4, 4, 128, 0),
+    ([1, 1, 1], [1, 40, 129], 16, 8, 2, 128, 0),
+    ([1, 1], [300, 5], 16, 8, 1, 64, 77),
+    ([1] * 9, [3, 1, 64, 65, 200, 16, 15, 33, 500], 32, 4, 1, 128, 16),
+    ([2, 0, 5, 1], [2, 0, 70, 130], 16, 6, 2, 64, 33),        # a sequence without tokens or keys
+    ([3, 1], [10, 2], 5, 4, 2, 64, 12),                       # pages that hold no whole 16 keys
+    ([4, 2], [90, 31], 1, 2, 1, 128, 3),                      # one key per page
+    ([8, 8, 3], [100, 8, 40], 64, 16, 16, 64, 130),
+    ([9, 17], [33, 17], 16, 28, 4, 128, 1),                   # 7 heads per kv head
+    ([40, 1, 23], [50, 300, 23], 16, 4, 2, 64, 200),          # several row tiles per sequence
+    ([1, 1], [2000, 1], 128, 4, 1, 64, 0),                    # many splits, and one key
+    ([2], [2], 256, 8, 8, 128, 3000),
+    ([65, 130], [65, 200], 64, 8, 2, 128, 300),
+    ([33], [400], 8, 4, 1, 64, 129),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PREFIX)))
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_prefix_attention(ra_lib, case, out_dtype):
+    n, lens, page, hq, hkv, d, plen = PREFIX[case]
+    x = Batch(n, lens, page, hkv, d, plen, seed=10 * case)
+    q = randn(x.N, hq, d, seed=10 * case + 7)
+    o, l = ra_lib.prefix_attn_fwd(q.to(DEV), *x.gpu("kp", "vp", "cu", "lens", "tables"), max(n),
+                                  max_len=max(max(lens), 1), prefix_table=x.ptable.to(DEV),
+                                  prefix_len=plen, out_dtype=out_dtype)
+    assert ra_lib.ra_sync_status() == 0
+    want = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, plen, d ** -0.5)
+    ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), f"case {case}")
+
+
+def test_rows_that_see_nothing(ra_lib):
+    """New tokens whose sequence has no key (length 0) and no prefix: 0 and -inf; a length
+    below the token count leaves the first tokens without own keys."""
+    x = Batch([2, 3, 1], [0, 2, 5], 16, 2, 64)
+    q = randn(x.N, 4, 64, seed=3)
+    o, l = ra_lib.prefix_attn_fwd(q.to(DEV), *x.gpu("kp", "vp", "cu", "lens", "tables"), 3,
+                                  max_len=5)
+    want = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, 0, 0.125)
+    assert (want[2][:, :3] == -float("inf")).all()
+    ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), "empty")
+
+
+def test_padded_batch_rows_stay(ra_lib):
+    """Rows behind the last sequence are left as they were, in every output."""
+    for plen in (0, 40):
+        x = Batch([1, 2], [20, 30], 16, 2, 64, plen, extra_rows=5)
+        q = randn(x.N, 4, 64, seed=5)
+        q[3:] = NAN
+        o = torch.full((x.N, 4, 64), 7.0, device=DEV)
+        l = torch.full((4, x.N), 7.0, device=DEV)
+        ra_lib.prefix_attn_fwd(q.to(DEV), *x.gpu("kp", "vp", "cu", "lens", "tables"), 2,
+                               max_len=30, prefix_table=x.ptable.to(DEV), prefix_len=plen, out=o,
+                               lse=l)
+        assert (o[3:] == 7).all() and (l[:, 3:] == 7).all()
+        want = ref.prefix_attention(q[:3], x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, plen,
+                                    0.125)
+        ref.check_attention(o[:3], l[:, :3].t(), (want[0], want[1], want[2].t()), "padded")
+
+
+def test_strided_queries_and_interleaved_pages(ra_lib):
+    """q as a slice of a wider projection; K and V pages interleaved in one allocation."""
+    x = Batch([3, 1], [50, 20], 16, 2, 64, 40, seed=2)
+    wide = randn(x.N, 10, 64, seed=9)
+    q = wide[:, 1:5]
+    kv = torch.stack([x.kp, x.vp], 1).to(DEV)
+    o, l = ra_lib.prefix_attn_fwd(wide.to(DEV)[:, 1:5], kv[:, 0], kv[:, 1],
+                                  *x.gpu("cu", "lens", "tables"), 3, max_len=50,
+                                  prefix_table=x.ptable.to(DEV), prefix_len=40)
+    want = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, 40, 0.125)
+    ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), "strided")
+
+
+def test_large_scores_and_extremes(ra_lib):
+    """Scores of some hundreds (one key takes nearly all the weight), and the same bits on
+    every call."""
+    x = Batch([2, 1], [70, 300], 16, 2, 64, 100, seed=4, fill=0.0)
+    q = randn(x.N, 4, 64, seed=1) * 64
+    args = (q.to(DEV), *x.gpu("kp", "vp", "cu", "lens", "tables"), 2)
+    kw = dict(max_len=300, prefix_table=x.ptable.to(DEV), prefix_len=100)
+    o, l = ra_lib.prefix_attn_fwd(*args, **kw)
+    o2, l2 = ra_lib.prefix_attn_fwd(*args, **kw)
+    assert torch.equal(o, o2) and torch.equal(l, l2)
+    # the scores' error grows with them: 64 times the unit case's 5.5e-5 is 3.5e-3, in the
+    # exponent, so a relative error of the weights of 2 * 3.5e-3 on top of the bf16 step
+    want = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, 100, 0.125)
+    tol = (ref.U + 7e-3) * (want[1] + want[0].abs())
+    assert ((o.double().cpu() - want[0]).abs() <= tol).all()
+    assert ((l.double().cpu() - want[2]).abs() <= 3.5e-3 + 2.0 ** -20 * want[2].abs()).all()
+
+
+def test_visible_nan_comes_through(ra_lib):
+    """A NaN in a key that a row sees is not swallowed by the softmax."""
+    x = Batch([1, 1], [40, 40], 16, 1, 64, seed=6)
+    x.kp[int(x.tables[0, 1]), 3] = NAN
+    q = randn(2, 1, 64, seed=2)
+    o, l = ra_lib.prefix_attn_fwd(q.to(DEV), *x.gpu("kp", "vp", "cu", "lens", "tables"), 1,
+                                  max_len=40)
+    assert torch.isnan(o[0]).all() and torch.isnan(l[:, 0]).all()
+    assert torch.isfinite(o[1]).all() and torch.isfinite(l[:, 1]).all()
+
+
+def test_indices_out_of_bounds_are_reported(ra_lib):
+    """Page ids, lengths and token counts outside their bounds are not followed; the next
+    ra_sync_status says so, once."""
+    x = Batch([1, 1], [20, 30], 16, 1, 64, seed=6, fill=0.0)
+    q = randn(2, 1, 64, seed=2).to(DEV)
+    k, v = randn(2, 1, 64, seed=3).to(DEV), randn(2, 1, 64, seed=4).to(DEV)
+    kp, vp, cu, lens, tables = x.gpu("kp", "vp", "cu", "lens", "tables")
+
+    def run(**kw):
+        a = dict(cu=cu, lens=lens, tables=tables) | kw
+        ra_lib.prefix_attn_fwd(q, kp, vp, a["cu"], a["lens"], a["tables"], 1, max_len=30)
+        first = ra_lib.load().ra_sync_status(None)
+        ra_lib.paged_kv_append(q, k, v, kp.clone(), vp.clone(), a["cu"], a["lens"], a["tables"],
+                               None, 1)
+        second = ra_lib.load().ra_sync_status(None)
+        assert ra_lib.load().ra_sync_status(None) == 0
+        return first, second
+
+    assert run() == (0, 0)
+    bad = tables.clone()
+    bad[1, 1] = x.n_pages
+    assert run(tables=bad) == (5, 5)
+    bad[1, 1] = -1
+    assert run(tables=bad) == (5, 5)
+    assert run(lens=i32([20, 33]).to(DEV)) == (5, 5)
+    assert run(lens=i32([20, 1 << 30]).to(DEV)) == (5, 5)
+    assert run(cu=i32([0, 2, 2]).to(DEV)) == (5, 5)
+    # a row count that is not sorted is cut at the tensor's rows
+    run(cu=i32([0, 1, 1 << 30]).to(DEV))
+    run(cu=i32([-5, 1, 2]).to(DEV))
+
+
+APPEND = [  # n, lens, page, hq, hkv, d, rot, interleaved, offset
+    ([1], [1], 16, 4, 2, 64, 64, False, 0),
+    ([1, 1, 1], [1, 17, 200], 16, 8, 2, 128, 128, False, 32768),
+    ([5, 0, 12, 1], [5, 0, 30, 9], 16, 4, 4, 64, 32, True, 1000003),
+    ([33, 2], [40, 2], 64, 6, 2, 128, 64, True, 7),
+    ([9], [9], 5, 2, 1, 64, 48, False, 123),
+    ([3, 4], [8, 4], 1, 7, 1, 128, 16, False, 2000000000),
+    ([6], [6], 16, 4, 2, 64, 0, False, 0),
+    ([130], [131], 32, 0, 3, 128, 128, False, 5),
+]
+
+
+@pytest.mark.parametrize("case", range(len(APPEND)))
+def test_append(ra_lib, case):
+    n, lens, page, hq, hkv, d, rot, inter, offset = APPEND[case]
+    x = Batch(n, lens, page, hkv, d, seed=20 * case, extra_rows=2)
+    wide = randn(x.N, hq + 2 * hkv, d, seed=3)
+    inv = (10000.0 ** (-torch.arange(0, rot, 2) / max(rot, 1))).float() if rot else None
+    dev = wide.to(DEV)
+    q, k, v = dev[:, :hq], dev[:, hq:hq + hkv], dev[:, hq + hkv:]
+    kp, vp = x.kp.to(DEV), x.vp.to(DEV)
+    q_out = torch.full((x.N, hq, d), 7.0, device=DEV).bfloat16() if hq else None
+    got = ra_lib.paged_kv_append(q if hq else None, k, v, kp, vp,
+                                 *x.gpu("cu", "lens", "tables"),
+                                 inv.to(DEV) if rot else None, max(n), pos_offset=offset,
+                                 interleaved=inter, q_out=q_out)
+    assert ra_lib.ra_sync_status() == 0
+    own = torch.cat([torch.arange(ln - m, ln) for m, ln in zip(n, lens)])
+    pos = own + offset
+    T = len(own)
+    rk = ref.rotate(wide[:T, hq:hq + hkv], pos, inv, inter)
+    want_k, want_v = x.kp.double(), x.vp.double()
+    size_k = torch.zeros_like(want_k)
+    half = rot // 2
+    i = torch.arange(half)
+    a, b = (2 * i, 2 * i + 1) if inter else (i, i + half)
+
+    def pair_size(t):  # |x| + |y| of the rotated pairs
+        z = torch.zeros(t.shape, dtype=torch.float64)
+        t = t.double().abs()
+        z[..., a] = z[..., b] = t[..., a] + t[..., b]
+        return z
+
+    sk = pair_size(wide[:T, hq:hq + hkv])
+    t = 0
+    for s, m in enumerate(n):
+        for _ in range(m):
+            w = (int(x.tables[s, int(own[t]) // page]), int(own[t]) % page)
+            want_k[w], want_v[w], size_k[w] = rk[t], wide[t, hq + hkv:].double(), sk[t]
+            t += 1
+    # every row of the cache: the written ones within half a bf16 step (plus the fp32 sine's
+    # and products' error, 2^-20 of the pair), all others and V bit for bit
+    assert torch.equal(vp.double().cpu().nan_to_num(9e9), want_v.nan_to_num(9e9))
+
+    def close(got, want, size):
+        got, want = got.double().cpu(), want
+        assert torch.equal(got.isnan(), want.isnan())
+        err = (got - want).abs().nan_to_num(0)
+        tol = (ref.U * (1 + 2.0 ** -10) * want.abs().nan_to_num(0) + 2.0 ** -20 * size)
+        tol[size == 0] = 0  # copied elements
+        assert (err <= tol).all(), float((err - tol).max())
+
+    close(kp, want_k, size_k)
+    if hq:
+        close(got[:T], ref.rotate(wide[:T, :hq], pos, inv, inter), pair_size(wide[:T, :hq]))
+        assert (got[T:] == 7).all()
+    else:
+        assert got is None
+
+
+def test_append_in_place_query(ra_lib):
+    x = Batch([3, 2], [9, 2], 16, 2, 64, seed=8)
+    q, k, v = (randn(5, h, 64, seed=h).to(DEV) for h in (4, 2, 2))
+    inv = torch.rand(32).to(DEV)
+    kp, vp = x.kp.to(DEV), x.vp.to(DEV)
+    args = (k, v, kp, vp, *x.gpu("cu", "lens", "tables"), inv, 3)
+    want = ra_lib.paged_kv_append(q, *args)
+    got = ra_lib.paged_kv_append(q, *args, q_out=q)
+    assert got is q and torch.equal(q, want)
+
+
+CROSS = [  # B, Lq, Lk, lens, hq, hkv, d
+    (1, 1, 1, [1], 1, 1, 64),
+    (3, 1, 50, [50, 0, 17], 4, 4, 64),
+    (2, 1, 1500, [1500, 3], 8, 2, 128),
+    (2, 3, 65, None, 6, 2, 64),
+    (2, 17, 200, [200, 130], 4, 1, 128),
+    (1, 130, 77, [70], 8, 8, 64),
+    (2, 300, 129, [129, 128], 2, 2, 128),
+    (3, 257, 640, [1, 0, 513], 7, 1, 64),
+]
+
+
+def cross_inputs(case, seed=0):
+    B, Lq, Lk, lens, hq, hkv, d = CROSS[case]
+    q = randn(B, Lq, hq, d, seed=seed + 1)
+    kv = randn(B, Lk, 2, hkv, d, seed=seed + 2)
+    for b, n in enumerate(lens or []):
+        kv[b, n:] = NAN
+    return q, kv, lens
+
+
+@pytest.mark.parametrize("case", range(len(CROSS)))
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_cross_attention(ra_lib, case, out_dtype):
+    q, kv, lens = cross_inputs(case, 30 * case)
+    dev = kv.to(DEV)
+    o, l = ra_lib.cross_attn_fwd(q.to(DEV), dev[:, :, 0], dev[:, :, 1],
+                                 kv_lens=i32(lens).to(DEV) if lens else None,
+                                 out_dtype=out_dtype)
+    assert ra_lib.ra_sync_status() == 0
+    want = ref.cross_attention(q, kv[:, :, 0], kv[:, :, 1], lens or [kv.shape[1]] * q.shape[0],
+                               q.shape[-1] ** -0.5)
+    ref.check_attention(o, l.transpose(1, 2), (want[0], want[1], want[2].transpose(1, 2)),
+                        f"case {case}")
+
+
+def test_decoder_step_together(ra_lib):
+    """Three decoder steps as a model runs them: append, attention behind the prefix over
+    the cache that the append filled, cross attention to the encoder's states."""
+    hq, hkv, d, page, plen = 4, 2, 64, 16, 37
+    x = Batch([0, 0, 0], [0, 0, 0], page, hkv, d, plen, seed=5, spare_pages=9, fill=0.0)
+    free = [p for p in range(x.n_pages) if p not in x.ptable.tolist()]
+    tables = i32(free[:6]).view(3, 2)
+    lens = i32([0, 0, 0])
+    kp, vp, pt = x.gpu("kp", "vp", "ptable")
+    inv = (10000.0 ** (-torch.arange(0, d, 2) / d)).float()
+    enc = randn(3, 29, 2, hkv, d, seed=50)
+    enc_len = [29, 1, 14]
+    ck, cv = x.kp.clone(), x.vp.clone()
+    for step, n in enumerate(([5, 1, 14], [1, 1, 1], [1, 1, 1])):
+        lens = lens + i32(n)
+        cu = i32([0, n[0], n[0] + n[1], sum(n)])
+        qkv = randn(sum(n), hq + 2 * hkv, d, seed=60 + step)
+        dev = qkv.to(DEV)
+        meta = (cu.to(DEV), lens.to(DEV), tables.to(DEV))
+        q = ra_lib.paged_kv_append(dev[:, :hq], dev[:, hq:hq + hkv], dev[:, hq + hkv:], kp, vp,
+                                   *meta, inv.to(DEV), max(n), pos_offset=plen)
+        o, l = ra_lib.prefix_attn_fwd(q, kp, vp, *meta, max(n), prefix_table=pt, prefix_len=plen,
+                                      out_dtype=torch.bfloat16)
+        want = ref.prefix_attention(q.cpu(), kp.cpu(), vp.cpu(), cu, lens, tables, x.ptable, plen,
+                                    d ** -0.5)
+        ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), f"step {step}")
+        if step:
+            e = enc.to(DEV)
+            c, cl = ra_lib.cross_attn_fwd(o[:, None], e[:, :, 0], e[:, :, 1],
+                                          kv_lens=i32(enc_len).to(DEV))
+            w = ref.cross_attention(o.cpu()[:, None], enc[:, :, 0], enc[:, :, 1], enc_len,
+                                    d ** -0.5)
+            ref.check_attention(c, cl.transpose(1, 2), (w[0], w[1], w[2].transpose(1, 2)), "cross")
+    # the cache holds every token's rotated key: the attention above read what was appended
+    own = kp.cpu()[tables[2].long()].flatten(0, 1)[:16]
+    assert (own != 0).any(-1).all() and torch.equal(kp.cpu()[x.ptable.long()],
+                                                    ck[x.ptable.long()])
+
+
+def test_side_stream_and_graph(ra_lib):
+    """On another stream than the current one, and captured: the graph follows device
+    lengths and tables that change between replays, and two graphs run side by side."""
+    x = Batch([1, 1], [20, 33], 16, 2, 64, 20, seed=11, fill=0.0)
+    q = randn(2, 4, 64, seed=12)
+    kp, vp, cu, lens, tables, pt = x.gpu("kp", "vp", "cu", "lens", "tables", "ptable")
+    qd = q.to(DEV)
+    kw = dict(max_len=64, prefix_table=pt, prefix_len=20)
+    wide = torch.cat([tables, tables], 1).contiguous()
+    want, wl = ra_lib.prefix_attn_fwd(qd, kp, vp, cu, lens, wide, 1, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, l = ra_lib.prefix_attn_fwd(qd, kp, vp, cu, lens, wide, 1, stream=side, **kw)
+    side.synchronize()
+    assert torch.equal(o, want) and torch.equal(l, wl)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = ra_lib.prefix_attn_fwd(qd, kp, vp, cu, lens, wide, 1, **kw)
+        graphs.append((g, res))
+    lens.copy_(i32([19, 7]))
+    s2 = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs[0][0].replay()
+    with torch.cuda.stream(s2):
+        graphs[1][0].replay()
+    torch.cuda.synchronize()
+    x.lens = i32([19, 7])
+    w = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, 20, 0.125)
+    for _, (o, l) in graphs:
+        ref.check_attention(o, l.t(), (w[0], w[1], w[2].t()), "graph")
+
+
+def test_offsets_past_32_bits(ra_lib):
+    """Pages whose element offset is past 2^32: a page stride of 2^28 elements, 17 pages in
+    one allocation of 9 GB, K and V interleaved; keys only in the last page."""
+    page, hkv, d = 16, 2, 64
+    stride = 1 << 28
+    buf = torch.empty(16 * stride + 2 * page * hkv * d, dtype=torch.bfloat16, device=DEV)
+    kv = buf.as_strided((17, 2, page, hkv, d), (stride, page * hkv * d, hkv * d, d, 1))
+    k, v = randn(page, hkv, d, seed=1), randn(page, hkv, d, seed=2)
+    qkv = randn(1, 4 + 2 * hkv, d, seed=3)
+    kv[16, 0], kv[16, 1] = k.to(DEV), v.to(DEV)
+    cu, lens, table = i32([0, 1]).to(DEV), i32([10]).to(DEV), i32([[16]]).to(DEV)
+    dev = qkv.to(DEV)
+    q = ra_lib.paged_kv_append(dev[:, :4], dev[:, 4:6], dev[:, 6:], kv[:, 0], kv[:, 1], cu, lens,
+                               table, None, 1)
+    o, l = ra_lib.prefix_attn_fwd(q, kv[:, 0], kv[:, 1], cu, lens, table, 1)
+    assert ra_lib.ra_sync_status() == 0
+    k[9], v[9] = qkv[0, 4:6], qkv[0, 6:]
+    assert torch.equal(kv[16, 0].cpu(), k) and torch.equal(kv[16, 1].cpu(), v)
+    w = ref.prefix_attention(qkv[:, :4], k[None], v[None], i32([0, 1]), i32([10]), i32([[0]]),
+                             i32([]), 0, 0.125)
+    ref.check_attention(o, l.t(), (w[0], w[1], w[2].t()), "far page")

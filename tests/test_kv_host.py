@@ -1,0 +1,112 @@
+"""Host side of the cache operators: every bad argument is refused before anything is
+launched (the pointers below are never dereferenced), and the workspace sizes are sane."""
+import ctypes
+
+import pytest
+import torch
+
+FAKE = 0x10000
+I64 = ctypes.c_longlong
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sequence_parallelism_attn_b200 import build, ra
+    build.build()
+    return ra.load()
+
+
+APPEND = dict(q=FAKE, k=FAKE, v=FAKE, qs=256, ks=128, vs=128, cu=FAKE, lens=FAKE, tables=FAKE,
+              inv=FAKE, B=2, N=4, T=2, hq=4, hkv=2, d=64, rot=64, inter=0, off=0, page=16, n=8,
+              mp=4, ps=2048, dt=0, qo=FAKE + 4096, qos=256, kp=FAKE, vp=FAKE)
+PREFIX = dict(q=FAKE, qs=256, kp=FAKE, vp=FAKE, cu=FAKE, lens=FAKE, tables=FAKE, pt=FAKE, plen=20,
+              B=2, N=4, T=2, max_len=64, hq=4, hkv=2, d=64, page=16, n=8, mp=4, ps=2048,
+              scale=0.125, dt=0, odt=0, out=FAKE, lse=FAKE, ws=FAKE, wsb=1 << 40)
+CROSS = dict(q=FAKE, k=FAKE, v=FAKE, lens=FAKE, B=2, Lq=3, Lk=50, hq=4, hkv=2, d=64, qt=256,
+             qb=768, kt=128, kb=6400, scale=0.125, dt=0, odt=0, out=FAKE, lse=FAKE, ws=FAKE,
+             wsb=1 << 40)
+
+
+def call(lib, entry, base, kw):
+    assert set(kw) <= set(base)
+    args = list((base | kw).values())
+    return getattr(lib, entry)(*args, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=0), 1), (dict(k=FAKE + 8), 1), (dict(v=0), 1), (dict(qo=0), 1), (dict(kp=FAKE + 2), 1),
+    (dict(cu=0), 1), (dict(lens=FAKE + 1), 1), (dict(tables=0), 1), (dict(inv=0), 1),
+    (dict(qs=248), 1), (dict(qs=260), 1), (dict(ks=127), 1), (dict(vs=64), 1), (dict(qos=200), 1),
+    (dict(B=0), 1), (dict(N=0), 1), (dict(T=0), 1), (dict(T=5), 1), (dict(hq=-1), 1),
+    (dict(hq=3), 1), (dict(hkv=0), 1), (dict(rot=8), 1), (dict(rot=80), 1), (dict(rot=-16), 1),
+    (dict(inter=2), 1), (dict(off=-1), 1), (dict(page=0), 1), (dict(n=0), 1), (dict(mp=0), 1),
+    (dict(ps=2040), 1), (dict(ps=2049), 1), (dict(d=96), 2), (dict(dt=1), 2), (dict(dt=7), 1),
+    (dict(N=1 << 25), 1), (dict(qo=FAKE, qos=512), 1),
+])
+def test_append_refusals(lib, kw, status):
+    assert call(lib, "ra_paged_kv_append", APPEND, kw) == status
+    assert lib.ra_last_error()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=0), 1), (dict(qs=264 - 16), 1), (dict(qs=257), 1), (dict(kp=0), 1),
+    (dict(vp=FAKE + 4), 1), (dict(cu=FAKE + 2), 1), (dict(lens=0), 1), (dict(tables=0), 1),
+    (dict(pt=0), 1), (dict(plen=-1), 1), (dict(B=0), 1), (dict(N=0), 1), (dict(T=9), 1),
+    (dict(max_len=0), 1), (dict(max_len=65), 1), (dict(hq=5), 1), (dict(d=32), 2),
+    (dict(page=0), 1), (dict(ps=100), 1), (dict(scale=0.0), 1), (dict(scale=float("inf")), 1),
+    (dict(scale=float("nan")), 1), (dict(dt=1), 2), (dict(odt=3), 1), (dict(out=0), 1),
+    (dict(lse=FAKE + 4), 1), (dict(ws=0), 1), (dict(ws=FAKE + 8), 1), (dict(wsb=16), 1),
+])
+def test_prefix_refusals(lib, kw, status):
+    assert call(lib, "ra_prefix_attn_fwd", PREFIX, kw) == status
+    assert lib.ra_last_error()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=0), 1), (dict(k=FAKE + 8), 1), (dict(v=0), 1), (dict(lens=FAKE + 2), 1),
+    (dict(B=0), 1), (dict(Lq=0), 1), (dict(Lk=0), 1), (dict(hq=3), 1), (dict(d=256), 2),
+    (dict(qt=255), 1), (dict(qb=700), 1), (dict(kt=130), 1), (dict(kb=6392), 1),
+    (dict(scale=-1.0), 1), (dict(dt=1), 2), (dict(odt=2), 1), (dict(out=FAKE + 2), 1),
+    (dict(lse=0), 1), (dict(B=1 << 13, Lq=1 << 13, qb=1 << 21), 1),
+])
+def test_cross_refusals(lib, kw, status):
+    assert call(lib, "ra_cross_attn_fwd", CROSS, kw) == status
+    assert lib.ra_last_error()
+
+
+def test_workspace_sizes(lib):
+    lib.ra_prefix_attn_workspace.restype = I64
+    # one split and no prefix: results are written without partials
+    assert lib.ra_prefix_attn_workspace(4, 4, 1, 100, 0, 8, 2, 64, 16) == 0
+    small = lib.ra_prefix_attn_workspace(4, 4, 1, 100, 1000, 8, 2, 64, 16)
+    assert small > 0 and small % (4 * 8 * 65 * 4) == 0
+    assert lib.ra_prefix_attn_workspace(0, 4, 1, 100, 0, 8, 2, 64, 16) == 0
+    assert lib.ra_cross_attn_workspace(1, 1, 100, 8, 2, 64) == 0
+    assert lib.ra_cross_attn_workspace(1, 1, 1 << 20, 8, 2, 64) > 0
+
+
+def test_binding_refusals():
+    """The Python helpers check shapes, types and layouts before the library is called."""
+    from sequence_parallelism_attn_b200 import ra
+    bf = dict(dtype=torch.bfloat16)
+    dev = torch.device("cpu")
+    pages = torch.zeros(4, 16, 2, 64, **bf)
+    with pytest.raises(ValueError):
+        ra._cache(pages, pages[:, :8], dev)
+    with pytest.raises(ValueError):
+        ra._cache(pages.float(), pages.float(), dev)
+    with pytest.raises(ValueError):
+        ra._cache(pages, torch.zeros(4, 2, 16, 2, 64, **bf)[:, 0], dev)
+    inter = torch.zeros(4, 2, 16, 2, 64, **bf)
+    assert ra._cache(inter[:, 0], inter[:, 1], dev) == (4, 16, 2, 64, 4096)
+    with pytest.raises(ValueError):
+        ra._ints(torch.zeros(3, dtype=torch.int64), "x", dev, (3,))
+    with pytest.raises(ValueError):
+        ra._ints(torch.zeros(3, dtype=torch.int32), "x", dev, (4,))
+    q, k = torch.zeros(2, 5, 4, 64, **bf), torch.zeros(2, 7, 2, 64, **bf)
+    assert ra._cross_strides(q, k, k) == (2, 5, 7, 4, 2, 64, 256, 1280, 128, 896)
+    for bad in ((q, k[:1], k[:1]), (q, k[..., :32], k[..., :32]), (q, k, k[:, :6]),
+                (q.float(), k, k), (q.transpose(1, 2), k, k),
+                (q, k, torch.zeros(2, 7, 4, 64, **bf)[:, :, :2])):
+        with pytest.raises(ValueError):
+            ra._cross_strides(*bad)
