@@ -536,6 +536,30 @@ RA_API ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v,
                                    void* workspace, long long workspace_bytes, void* stream);
 
 /*
+ * ra_cross_attn_bwd -- the gradients of ra_cross_attn_fwd's out with respect to q, k and v
+ * given dout (the formulas of ra_ring_attn_bwd over the keys j < kv_lens[b]; with grouped
+ * heads dk and dv are the sums over the group).  Rows of dk and dv past kv_lens[b] are zero,
+ * and so is dq of a batch row without keys.
+ *   q, k, v, kv_lens, sizes, strides, scale   as given to ra_cross_attn_fwd.
+ *   out, dout  device bf16, dense [B][Lq][H_q][D]: the forward's output, and the gradient.
+ *   lse        device fp32, [B][H_q][Lq]: the forward's.
+ *   grad_dtype RA_FP32 or RA_BF16 (sums in fp32, rounded once): dq dense [B][Lq][H_q][D],
+ *              dk, dv dense [B][Lk][H_kv][D].
+ *   workspace  device, 16-byte aligned, at least ra_cross_attn_bwd_workspace(...) bytes.
+ * Reproducibility and ra_set_bwd_deterministic: as ra_ring_attn_bwd.
+ * Errors: as ra_cross_attn_fwd.
+ */
+RA_API long long ra_cross_attn_bwd_workspace(int B, int Lq, int H_q, int D, ra_dtype grad_dtype);
+RA_API ra_status ra_cross_attn_bwd(const void* q, const void* k, const void* v,
+                                   const int* kv_lens, const void* out, const float* lse,
+                                   const void* dout, int B, int Lq, int Lk, int H_q, int H_kv,
+                                   int D, long long q_tstride, long long q_bstride,
+                                   long long kv_tstride, long long kv_bstride, float scale,
+                                   ra_dtype in_dtype, ra_dtype grad_dtype, void* dq, void* dk,
+                                   void* dv, void* workspace, long long workspace_bytes,
+                                   void* stream);
+
+/*
  * ra_sync_status -- synchronise `stream`, then read and clear this device's
  * kernel error word.  Returns RA_ERR_TIMEOUT if a kernel launched since the
  * last call gave up on a bounded wait, RA_ERR_INDEX if one met an index outside
@@ -555,7 +579,8 @@ RA_API unsigned long long ra_set_wait_limit_ns(unsigned long long ns);
 
 /*
  * ra_set_bwd_deterministic -- process-wide switch of every backward entry point
- * (ra_ring_attn_bwd and its _accumulate, _static, _zigzag and _packed forms).  With on != 0
+ * (ra_ring_attn_bwd and its _accumulate, _static, _zigzag and _packed forms, and
+ * ra_cross_attn_bwd).  With on != 0
  * the gradients are bitwise reproducible: dq comes from a kernel that keeps a query
  * tile stationary, visits the key tiles it sees in one fixed order and writes each dq
  * element once (adding it into dq in the _accumulate form), and the key-stationary

@@ -120,3 +120,33 @@ def usp_attention_dist(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal
         scale = q.shape[-1] ** -0.5
     return _USPAttentionDist.apply(q.contiguous(), k.contiguous(), v.contiguous(), bool(causal),
                                    float(scale), ulysses_group, ring_group)
+
+
+class _CrossAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, kv_lens, scale):
+        o, lse = ra.cross_attn_fwd(q, k, v, kv_lens, scale, out_dtype=q.dtype)
+        ctx.save_for_backward(q, k, v, o, lse, kv_lens)
+        ctx.scale = scale
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, kv_lens = ctx.saved_tensors
+        dq, dk, dv = ra.cross_attn_bwd(q, k, v, o, lse, do.to(q.dtype).contiguous(), kv_lens,
+                                       ctx.scale, grad_dtype=q.dtype)
+        return dq, dk, dv, None, None
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    kv_lens: torch.Tensor | None = None,
+                    scale: float | None = None) -> torch.Tensor:
+    """Cross attention with autograd: q [B, Lq, H_q, D] to an encoder's states k, v
+    [B, Lk, H_kv, D] (bf16; slices of one projection are taken as they are), per batch row
+    the first kv_lens[b] of them (int32 [B], None: all) -> O [B, Lq, H_q, D] bf16.
+    backward() gives dq, dk, dv in bf16 (summed in fp32, rounded once)."""
+    if q.dtype != torch.bfloat16:
+        raise ValueError("the differentiable path takes bf16 inputs (the tensor-core backward)")
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    return _CrossAttention.apply(q, k, v, kv_lens, float(scale))

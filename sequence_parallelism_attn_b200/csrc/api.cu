@@ -37,6 +37,8 @@ int elem_size(ra_dtype d) { return d == RA_BF16 ? 2 : (d == RA_FP32 ? 4 : 0); }
 
 namespace ra {
 int set_last_error(int status, const std::string& msg) { return (int)fail((ra_status)status, msg); }
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
+int bwd_deterministic() { return g_bwd_deterministic.load(); }
 }  // namespace ra
 
 extern "C" {

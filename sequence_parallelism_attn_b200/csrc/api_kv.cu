@@ -224,16 +224,17 @@ long long ra_cross_attn_workspace(int B, int Lq, int Lk, int H_q, int H_kv, int 
     return ra::plan_kv_rows(B, B * Lq, Lq, Lk, 0, H_q, H_kv, D).workspace;
 }
 
-ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v, const int* kv_lens, int B,
-                            int Lq, int Lk, int H_q, int H_kv, int D, long long q_tstride,
-                            long long q_bstride, long long kv_tstride, long long kv_bstride,
-                            float scale, ra_dtype in_dtype, ra_dtype out_dtype, void* out,
-                            float* lse, void* workspace, long long workspace_bytes, void* stream) {
+// The sizes and strides that cross attention's forward and backward share.
+static ra_status check_cross(const void* q, const void* k, const void* v, const int* kv_lens,
+                             int B, int Lq, int Lk, int H_q, int H_kv, int D, long long q_tstride,
+                             long long q_bstride, long long kv_tstride, long long kv_bstride,
+                             ra_dtype in_dtype) {
     RA_CHECK(check_heads(H_q, H_kv, D, in_dtype));
     if (B < 1 || Lq < 1 || Lk < 1) return fail(RA_ERR_INVALID, "B, Lq and Lk must be >= 1");
     if ((long long)B * Lq > kMaxTokens || Lk > kMaxKeys)
         return fail(RA_ERR_INVALID, "B * Lq must be <= 2^24 and Lk <= 2^30");
-    RA_CHECK(check_results(scale, out_dtype, out, lse));
+    if ((long long)B * Lq * H_q > 0x7fffffffLL)
+        return fail(RA_ERR_INVALID, "problem too large for one launch");
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
         return fail(RA_ERR_INVALID, "q, k and v must be non-null and 16-byte aligned");
     if (kv_lens && !aligned(kv_lens, 4))
@@ -241,7 +242,17 @@ ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v, const i
     RA_CHECK(check_stride(q_tstride, (long long)H_q * D, "q_tstride"));
     RA_CHECK(check_stride(kv_tstride, (long long)H_kv * D, "kv_tstride"));
     RA_CHECK(check_stride(q_bstride, (Lq - 1) * q_tstride + (long long)H_q * D, "q_bstride"));
-    RA_CHECK(check_stride(kv_bstride, (Lk - 1) * kv_tstride + (long long)H_kv * D, "kv_bstride"));
+    return check_stride(kv_bstride, (Lk - 1) * kv_tstride + (long long)H_kv * D, "kv_bstride");
+}
+
+ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v, const int* kv_lens, int B,
+                            int Lq, int Lk, int H_q, int H_kv, int D, long long q_tstride,
+                            long long q_bstride, long long kv_tstride, long long kv_bstride,
+                            float scale, ra_dtype in_dtype, ra_dtype out_dtype, void* out,
+                            float* lse, void* workspace, long long workspace_bytes, void* stream) {
+    RA_CHECK(check_cross(q, k, v, kv_lens, B, Lq, Lk, H_q, H_kv, D, q_tstride, q_bstride,
+                         kv_tstride, kv_bstride, in_dtype));
+    RA_CHECK(check_results(scale, out_dtype, out, lse));
     ra::KvArgs a;
     a.q = q;
     a.q_tstride = q_tstride;
@@ -274,10 +285,63 @@ ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v, const i
     a.stream = (cudaStream_t)stream;
     const ra::KvPlan plan = ra::plan_kv_rows(B, B * Lq, Lq, Lk, 0, H_q, H_kv, D);
     RA_CHECK(check_workspace(workspace, workspace_bytes, plan.workspace));
-    if ((long long)B * Lq * H_q > 0x7fffffffLL || plan.blocks > 0x7fffffffLL)
+    if (plan.blocks > 0x7fffffffLL)
         return fail(RA_ERR_INVALID, "problem too large for one launch");
     const cudaError_t e = ra::launch_kv_rows(a, plan);
     return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross attention launch");
+}
+
+long long ra_cross_attn_bwd_workspace(int B, int Lq, int H_q, int D, ra_dtype grad_dtype) {
+    if (B < 1 || Lq < 1 || H_q < 1 || D < 1) return 0;
+    const long long rows = ((long long)B * Lq * H_q + 3) / 4 * 4;
+    return 4 * (rows + (grad_dtype == RA_BF16 ? rows * D : 0));
+}
+
+ra_status ra_cross_attn_bwd(const void* q, const void* k, const void* v, const int* kv_lens,
+                            const void* out, const float* lse, const void* dout, int B, int Lq,
+                            int Lk, int H_q, int H_kv, int D, long long q_tstride,
+                            long long q_bstride, long long kv_tstride, long long kv_bstride,
+                            float scale, ra_dtype in_dtype, ra_dtype grad_dtype, void* dq,
+                            void* dk, void* dv, void* workspace, long long workspace_bytes,
+                            void* stream) {
+    RA_CHECK(check_cross(q, k, v, kv_lens, B, Lq, Lk, H_q, H_kv, D, q_tstride, q_bstride,
+                         kv_tstride, kv_bstride, in_dtype));
+    RA_CHECK(check_results(scale, grad_dtype, out, lse));
+    if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16))
+        return fail(RA_ERR_INVALID, "dout, dq, dk and dv must be non-null and 16-byte aligned");
+    if ((long long)B * H_kv * ((Lk + 127) / 128) > 0x7fffffffLL)
+        return fail(RA_ERR_INVALID, "problem too large for one launch");
+    RA_CHECK(check_workspace(workspace, workspace_bytes,
+                             ra_cross_attn_bwd_workspace(B, Lq, H_q, D, grad_dtype)));
+    ra::CrossBwdArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.out = out;
+    a.dout = dout;
+    a.lse = lse;
+    a.kv_lens = kv_lens;
+    a.B = B;
+    a.Lq = Lq;
+    a.Lk = Lk;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.q_tstride = q_tstride;
+    a.q_bstride = q_bstride;
+    a.kv_tstride = kv_tstride;
+    a.kv_bstride = kv_bstride;
+    a.scale = scale;
+    a.grad_bf16 = grad_dtype == RA_BF16;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.workspace = (float*)workspace;
+    a.stream = (cudaStream_t)stream;
+    const char* why = "cross attention backward launch";
+    const cudaError_t e =
+        ra::launch_cross_bwd(a, ra::wait_limit_ns(), ra::bwd_deterministic(), &why);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, why);
 }
 
 }  // extern "C"

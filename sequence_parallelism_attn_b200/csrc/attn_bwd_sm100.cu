@@ -71,13 +71,23 @@ struct __align__(64) BwdParams {
     int accumulate;   // dK, dV added to the values in memory (dQ: not zeroed by Delta)
     int skip_dq;      // deterministic mode: dQ from bwd_dq_sm100 (the key-stationary kernel
                       // is then its SKIP_DQ instance)
+    const int* kv_lens;  // cross attention: keys per batch row (null: Lc)
+    int grad_bf16;       // cross attention: dK, dV written in bf16
     float scale, scale_log2;
     unsigned long long wait_limit_ns;
 };
 
 // Shard layouts, compiled as separate kernels (the contiguous one keeps plain index
-// arithmetic per tile).
-constexpr int kLayoutContiguous = 0, kLayoutZigzag = 1, kLayoutPacked = 2;
+// arithmetic per tile).  Cross attention is the contiguous form without causal order whose
+// L query rows and Lc keys differ in number (P = 1), with a key count per batch row.
+constexpr int kLayoutContiguous = 0, kLayoutZigzag = 1, kLayoutPacked = 2, kLayoutCross = 3;
+
+// Cross attention: the keys of batch row b.
+__device__ __forceinline__ int cross_keys(const BwdParams& p, int b) {
+    if (!p.kv_lens) return p.Lc;
+    const int n = p.kv_lens[b];
+    return n < 0 ? 0 : (n > p.Lc ? p.Lc : n);
+}
 
 
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, unsigned code) {
@@ -310,6 +320,19 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const uint16_t* __restri
     }
 }
 
+// One warp zeroes rows first .. 127 of two adjacent 128 x D tiles (128-byte swizzle blocks:
+// a row of a block is 128 consecutive bytes whatever the swizzle).  Keys past a batch row's
+// count may hold anything; as zeros they add nothing to products that P = dS = 0 weigh (a
+// NaN would).  The caller's fence orders the stores before the tensor core's reads.
+template <int D>
+__device__ __forceinline__ void zero_key_rows(uint32_t tiles, int first) {
+    constexpr int BLK = kBM * 128;
+    const int lane = threadIdx.x & 31, n16 = (kBN - first) * 8;  // 16-byte pieces per block
+    for (int blk = 0; blk < 2 * (D / 64); ++blk)
+        for (int i = lane; i < n16; i += 32)
+            st_shared_v4(tiles + blk * BLK + first * 128 + i * 16, 0, 0, 0, 0);
+}
+
 template <int D>
 struct QCfg {
     static constexpr int TILE = kBM * D * 2;  // bytes of a 128 x D bf16 tile
@@ -409,9 +432,16 @@ __global__ void __launch_bounds__(kThreadsQ, 1) bwd_dq_sm100(const __grid_consta
         fence_mbar_init();
         fence_proxy_async_smem();
     }
+    constexpr bool CROSS = LAYOUT == kLayoutCross;
+    const int n_keys = CROSS ? cross_keys(p, b) : p.Lc;
+    const uint32_t land = bar(C::N_BARS - 1);  // cross: the partial tile's bytes have landed
+    if (CROSS && threadIdx.x == 0) {
+        mbar_init(land, 1);
+        fence_mbar_init();
+    }
     if (warp == kWarpLoad) {
         SchedArgs sa;
-        sa.P = p.P; sa.Lc = p.Lc; sa.L = p.L; sa.causal = p.causal;
+        sa.P = p.P; sa.Lc = n_keys; sa.L = p.L; sa.causal = p.causal;
         sa.zigzag = LAYOUT == kLayoutZigzag ? 1 : 0;
         sa.pid = LAYOUT == kLayoutPacked ? p.pid : nullptr;
         const long long last_row = min((long long)r0 + kBM - 1, (long long)p.L - 1);
@@ -434,6 +464,11 @@ __global__ void __launch_bounds__(kThreadsQ, 1) bwd_dq_sm100(const __grid_consta
     const int n = *n_slot;
 
     if (warp == kWarpLoad) {
+        // cross: the last tile ends inside the states, with rows of other content behind it
+        const int part = CROSS && n > 0 && n * kBN > n_keys && n_keys < p.Lc ? 1 : 0;
+        int go = 1;
+        int armed[C::NS];
+        for (int s = 0; s < C::NS; ++s) armed[s] = -1;
         if (lane == 0) {
             // Q and dO once; K and V of each visited tile through an NS-deep ring
             mbar_arrive_expect_tx(bar(C::BAR_FIXED), 2 * C::TILE);
@@ -441,15 +476,16 @@ __global__ void __launch_bounds__(kThreadsQ, 1) bwd_dq_sm100(const __grid_consta
                 tma_load_4d(base + C::OFF_A + kb * C::BLK, &p.tm_q, bar(C::BAR_FIXED), kb * 64, h, r0, b);
                 tma_load_4d(base + C::OFF_B + kb * C::BLK, &p.tm_do, bar(C::BAR_FIXED), kb * 64, h, r0, b);
             }
-            int armed[C::NS];
-            for (int s = 0; s < C::NS; ++s) armed[s] = -1;
             SchedIter it;
             it.begin(sched);
-            for (int jt = 0; jt < n; ++jt, it.next()) {
+            const int n_loop = n - part;
+            for (int jt = 0; jt < n_loop; ++jt, it.next()) {
                 const int slot = jt % C::NS;
                 if (jt >= C::NS &&
-                    !wait1(bar(C::bar_empty(slot)), ((jt / C::NS) - 1) & 1, abort_flag, lim, kErrLoad))
+                    !wait1(bar(C::bar_empty(slot)), ((jt / C::NS) - 1) & 1, abort_flag, lim, kErrLoad)) {
+                    if (CROSS) go = 0;
                     break;
+                }
                 const uint32_t st = base + C::OFF_RING + slot * C::STAGE;
                 mbar_arrive_expect_tx(bar(C::bar_full(slot)), 2 * C::TILE);
                 for (int kb = 0; kb < C::NKB; ++kb) {
@@ -460,9 +496,47 @@ __global__ void __launch_bounds__(kThreadsQ, 1) bwd_dq_sm100(const __grid_consta
                 }
                 armed[slot] = jt;
             }
+            if (CROSS && part && go) {
+                const int jt = n - 1, slot = jt % C::NS;
+                if (jt >= C::NS &&
+                    !wait1(bar(C::bar_empty(slot)), ((jt / C::NS) - 1) & 1, abort_flag, lim, kErrLoad)) {
+                    go = 0;
+                } else {
+                    const uint32_t st = base + C::OFF_RING + slot * C::STAGE;
+                    mbar_arrive_expect_tx(land, 2 * C::TILE);
+                    for (int kb = 0; kb < C::NKB; ++kb) {
+                        tma_load_4d(st + kb * C::BLK, &p.tm_k[0], land, kb * 64, g, jt * kBN, b);
+                        tma_load_4d(st + C::TILE + kb * C::BLK, &p.tm_v[0], land, kb * 64, g,
+                                    jt * kBN, b);
+                    }
+                    go = 2;
+                }
+            }
             wait_drain(bar(C::BAR_FIXED), 0, abort_flag, lim);
-            for (int s = 0; s < C::NS; ++s)
-                if (armed[s] >= 0) wait_drain(bar(C::bar_full(s)), (armed[s] / C::NS) & 1, abort_flag, lim);
+            if (!CROSS)
+                for (int s = 0; s < C::NS; ++s)
+                    if (armed[s] >= 0) wait_drain(bar(C::bar_full(s)), (armed[s] / C::NS) & 1, abort_flag, lim);
+        }
+        if (CROSS) {
+            // the partial tile: its bytes land on a barrier of their own, the warp zeroes
+            // the rows past the batch row's keys, then the tile is published as the others are
+            go = __shfl_sync(0xffffffffu, go, 0);
+            if (go == 2) {
+                const int slot = (n - 1) % C::NS;
+                const bool landed = wait_warp(land, 0, abort_flag, lim, kErrLoad);
+                if (!landed && lane == 0) wait_drain(land, 0, abort_flag, lim);
+                __syncwarp();
+                if (landed) {
+                    zero_key_rows<D>(base + C::OFF_RING + slot * C::STAGE, n_keys - (n - 1) * kBN);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::bar_full(slot)));
+                    armed[slot] = n - 1;  // the drain below waits for this, the last, phase
+                }
+            }
+            if (lane == 0)
+                for (int s = 0; s < C::NS; ++s)
+                    if (armed[s] >= 0) wait_drain(bar(C::bar_full(s)), (armed[s] / C::NS) & 1, abort_flag, lim);
         }
     } else if (warp == kWarpMma || warp == kWarpMma2) {
         if (lane == 0) {
@@ -586,10 +660,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1) bwd_dq_sm100(const __grid_consta
             }
             __syncwarp();
             tc_fence_after();
-            const int kvalid = min(kBN, p.Lc - it.t * kBN);
+            const int kvalid = min(kBN, n_keys - it.t * kBN);
             // this row sees the tile's keys c with c_lo <= c <= c_hi
             int c_lo = -1, c_hi;
-            if (LAYOUT == kLayoutContiguous) {
+            if (LAYOUT == kLayoutContiguous || CROSS) {
                 const long long k0 = (long long)it.chunk() * p.Lc + (long long)it.t * kBN;
                 const long long lim = p.causal ? my_row - k0 : (long long)kBN;
                 c_hi = (int)min((long long)(kvalid - 1), lim < -1 ? -1LL : lim);
@@ -764,7 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
     auto bar = [&](int i) { return base + C::OFF_BAR + 8u * (uint32_t)i; };
     const unsigned long long lim = p.wait_limit_ns;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr bool CONTIG = LAYOUT == kLayoutContiguous;
+    constexpr bool CROSS = LAYOUT == kLayoutCross;
+    constexpr bool CONTIG = LAYOUT == kLayoutContiguous || CROSS;
 
     // grid: (batch, kv head) outermost, then the key tiles (chunk j, tile t) heaviest first
     const int n_kt = p.P * p.ntc;
@@ -777,7 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
         t = (seg < p.P ? 0 : seg_tiles) + kt % seg_tiles;
     }
     const long long key0 = (long long)j * p.Lc + (long long)t * kBN;
-    const int kvalid = min(kBN, p.Lc - t * kBN);
+    const int kvalid = min(kBN, (CROSS ? cross_keys(p, b) : p.Lc) - t * kBN);  // cross: may be < 1
+    const uint32_t land = base + C::OFF_QR;  // cross: K and V of a partial tile have landed
     const int qt0 = p.causal ? (int)(key0 / kBM) : 0;
     const int n_qt = p.n_qblocks - qt0;
 
@@ -799,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
         mbar_init(bar(C::BAR_DQREADY), 1);
         mbar_init(bar(C::BAR_ACC), 2);    // dV from A, dK from B
         mbar_init(bar(C::BAR_DRAIN), 3);  // A, B, C
+        if (CROSS) mbar_init(land, 1);
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -819,7 +896,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int n = CONTIG ? n_qt * p.group : *n_slot;  // (head, query tile) items, head-major
+    // (head, query tile) items, head-major; a cross tile past the batch row's keys has none
+    const int n = CONTIG ? (CROSS && kvalid < 1 ? 0 : n_qt * p.group) : *n_slot;
 
     // the items in order: (query head, first row of the query tile)
     auto for_items = [&](auto&& fn) {
@@ -847,12 +925,27 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
     if (warp >= kComputeWarps && warp < kWarpRed0) {
       regs_decrease<kRegsOther>();
       if (warp == kWarpLoad) {
+        // cross: rows of the states past the batch row's keys share the tile; they are zeroed
+        // once the tile has landed, before it is published
+        const bool part = CROSS && n > 0 && kvalid < kBN && t * kBN + kvalid < p.Lc;
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar(C::BAR_FIXED), 2 * C::TILE);
+            const uint32_t fb = part ? land : bar(C::BAR_FIXED);
+            mbar_arrive_expect_tx(fb, 2 * C::TILE);
             for (int kb = 0; kb < C::NKB; ++kb) {
-                tma_load_4d(base + C::OFF_A + kb * C::BLK, &p.tm_k[j], bar(C::BAR_FIXED), kb * 64, g, t * kBN, b);
-                tma_load_4d(base + C::OFF_B + kb * C::BLK, &p.tm_v[j], bar(C::BAR_FIXED), kb * 64, g, t * kBN, b);
+                tma_load_4d(base + C::OFF_A + kb * C::BLK, &p.tm_k[j], fb, kb * 64, g, t * kBN, b);
+                tma_load_4d(base + C::OFF_B + kb * C::BLK, &p.tm_v[j], fb, kb * 64, g, t * kBN, b);
             }
+        }
+        if (CROSS && part) {
+            const bool landed = wait_warp(land, 0, abort_flag, lim, kErrLoad);
+            if (!landed && lane == 0) wait_drain(land, 0, abort_flag, lim);
+            __syncwarp();
+            if (landed) {
+                zero_key_rows<D>(base + C::OFF_A, kvalid);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::BAR_FIXED));
         }
         int armed[C::NS];
         for (int s = 0; s < C::NS; ++s) armed[s] = -1;
@@ -1244,6 +1337,34 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
                 uint32_t o[32];
                 tmem_ld32(tmem + lane_off + C::COL_DV + which * D + cb * 32, o);
                 tmem_wait_ld();
+                if (CROSS) {
+                    // every row of the states is written, zeros past the batch row's keys
+                    if (t * kBN + key_t < p.Lc) {
+                        const float m = key_ok ? mul : 0.f;
+                        if (p.grad_bf16) {
+                            uint4* dst = reinterpret_cast<uint4*>(
+                                reinterpret_cast<uint16_t*>(outp) + orow + cb * 32);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * m,
+                                                       __uint_as_float(o[8 * i + 2 * e + 1]) * m);
+                                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(outp + orow + cb * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[i] = make_float4(__uint_as_float(o[4 * i]) * m,
+                                                     __uint_as_float(o[4 * i + 1]) * m,
+                                                     __uint_as_float(o[4 * i + 2]) * m,
+                                                     __uint_as_float(o[4 * i + 3]) * m);
+                        }
+                    }
+                    continue;
+                }
                 if (key_ok) {
                     float4* dst = reinterpret_cast<float4*>(outp + orow + cb * 32);
 #pragma unroll
@@ -1262,6 +1383,16 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
                         dst[i] = r;
                     }
                 }
+            }
+        } else if (CROSS && ok && n == 0) {  // past the batch row's keys
+            if (t * kBN + key_t < p.Lc) {
+                const long long orow = (((long long)b * p.Lc + t * kBN + key_t) * p.H_kv + g) * D;
+                float* outp = c ? p.dk[j] : p.dv[j];
+                uint4* dst = p.grad_bf16 ? reinterpret_cast<uint4*>(
+                                               reinterpret_cast<uint16_t*>(outp) + orow)
+                                         : reinterpret_cast<uint4*>(outp + orow);
+                const int n16 = D * (p.grad_bf16 ? 2 : 4) / 16;
+                for (int i = 0; i < n16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
             }
         } else if (ok && n == 0 && key_ok && !p.accumulate) {  // no query sees the key
             const long long orow = (((long long)b * p.Lc + t * kBN + key_t) * p.H_kv + g) * D;
@@ -1294,11 +1425,12 @@ PFN_cuTensorMapEncodeTiled_v12000 bwd_encode_fn() {
 
 // [D][H][rows][B] bf16 tensor, 128-row x 64-column boxes, 128-byte swizzle, zero fill.
 bool bwd_tile_map(CUtensorMap* m, const void* ptr, int D, int H, long long rows, int B,
-                  long long bstride_elems) {
+                  long long bstride_elems, long long tstride_elems = 0) {
     auto enc = bwd_encode_fn();
     if (!enc) return false;
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows, (cuuint64_t)B};
-    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)bstride_elems * 2};
+    const long long ts = tstride_elems ? tstride_elems : (long long)H * D;
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)ts * 2, (cuuint64_t)bstride_elems * 2};
     cuuint32_t box[4] = {64, 1, (cuuint32_t)kBM, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
@@ -1329,16 +1461,16 @@ cudaError_t launch_bwd_d(const BwdParams& p, const AttnBwdArgs& a, const char** 
     if (e != cudaSuccess) return e;
     // [skip dQ][layout]: the deterministic mode's key-stationary kernel is compiled apart,
     // so that the default one carries no test of it
-    decltype(&bwd_sm100<D, kLayoutContiguous, false>) kern[2][3] = {
+    decltype(&bwd_sm100<D, kLayoutContiguous, false>) kern[2][4] = {
         {bwd_sm100<D, kLayoutContiguous, false>, bwd_sm100<D, kLayoutZigzag, false>,
-         bwd_sm100<D, kLayoutPacked, false>},
+         bwd_sm100<D, kLayoutPacked, false>, bwd_sm100<D, kLayoutCross, false>},
         {bwd_sm100<D, kLayoutContiguous, true>, bwd_sm100<D, kLayoutZigzag, true>,
-         bwd_sm100<D, kLayoutPacked, true>}};
-    decltype(&bwd_dq_sm100<D, kLayoutContiguous>) kern_dq[3] = {
+         bwd_sm100<D, kLayoutPacked, true>, bwd_sm100<D, kLayoutCross, true>}};
+    decltype(&bwd_dq_sm100<D, kLayoutContiguous>) kern_dq[4] = {
         bwd_dq_sm100<D, kLayoutContiguous>, bwd_dq_sm100<D, kLayoutZigzag>,
-        bwd_dq_sm100<D, kLayoutPacked>};
+        bwd_dq_sm100<D, kLayoutPacked>, bwd_dq_sm100<D, kLayoutCross>};
     if (configured_for != dev) {
-        for (int l = 0; l < 3; ++l) {
+        for (int l = 0; l < 4; ++l) {
             for (int sk = 0; sk < 2; ++sk) {
                 // the register split assumes the launch allocation: a raise beyond it
                 // would never complete
@@ -1359,7 +1491,9 @@ cudaError_t launch_bwd_d(const BwdParams& p, const AttnBwdArgs& a, const char** 
         }
         configured_for = dev;
     }
-    const int layout = p.pid ? kLayoutPacked : (p.zigzag ? kLayoutZigzag : kLayoutContiguous);
+    const int layout = a.cross_Lq ? kLayoutCross
+                       : p.pid    ? kLayoutPacked
+                                  : (p.zigzag ? kLayoutZigzag : kLayoutContiguous);
     const long long rows = (long long)a.B * p.L * a.H_q;
     bwd_delta_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, a.stream>>>(
         (const uint16_t*)a.out, (const uint16_t*)a.dout, a.workspace, a.dq,
@@ -1381,8 +1515,8 @@ cudaError_t launch_bwd_d(const BwdParams& p, const AttnBwdArgs& a, const char** 
 cudaError_t launch_attn_bwd_sm100(const AttnBwdArgs& a, unsigned long long wait_limit_ns,
                                   const char** why) {
     static thread_local BwdParams p;
-    const long long L = (long long)a.P * a.Lc;
-    if (!bwd_tile_map(&p.tm_q, a.q, a.D, a.H_q, L, a.B, a.q_bstride) ||
+    const long long L = a.cross_Lq ? a.cross_Lq : (long long)a.P * a.Lc;
+    if (!bwd_tile_map(&p.tm_q, a.q, a.D, a.H_q, L, a.B, a.q_bstride, a.q_tstride) ||
         !bwd_tile_map(&p.tm_do, a.dout, a.D, a.H_q, L, a.B, L * a.H_q * a.D)) {
         *why = "cuTensorMapEncodeTiled failed for q or dout";
         return cudaErrorInvalidValue;
@@ -1392,8 +1526,10 @@ cudaError_t launch_attn_bwd_sm100(const AttnBwdArgs& a, unsigned long long wait_
         return cudaErrorInvalidValue;
     }
     for (int j = 0; j < a.P; ++j) {
-        if (!bwd_tile_map(&p.tm_k[j], a.k_chunks[j], a.D, a.H_kv, a.Lc, a.B, a.kv_bstride) ||
-            !bwd_tile_map(&p.tm_v[j], a.v_chunks[j], a.D, a.H_kv, a.Lc, a.B, a.kv_bstride)) {
+        if (!bwd_tile_map(&p.tm_k[j], a.k_chunks[j], a.D, a.H_kv, a.Lc, a.B, a.kv_bstride,
+                          a.kv_tstride) ||
+            !bwd_tile_map(&p.tm_v[j], a.v_chunks[j], a.D, a.H_kv, a.Lc, a.B, a.kv_bstride,
+                          a.kv_tstride)) {
             *why = "cuTensorMapEncodeTiled failed for a K/V chunk";
             return cudaErrorInvalidValue;
         }
@@ -1415,6 +1551,8 @@ cudaError_t launch_attn_bwd_sm100(const AttnBwdArgs& a, unsigned long long wait_
     p.pid = a.pid;
     p.accumulate = a.accumulate;
     p.skip_dq = a.deterministic ? 1 : 0;
+    p.kv_lens = a.kv_lens;
+    p.grad_bf16 = a.grad_bf16;
     p.group = a.H_q / a.H_kv;
     p.n_qblocks = (int)((L + kBM - 1) / kBM);
     p.ntc = (a.Lc + kBN - 1) / kBN;

@@ -61,6 +61,21 @@ struct KvPlan {
 KvPlan plan_kv_rows(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
                     int H_kv, int D);
 cudaError_t launch_kv_rows(const KvArgs& a, const KvPlan& p);
+
+struct CrossBwdArgs {
+    const void *q, *k, *v, *out, *dout;
+    const float* lse;
+    const int* kv_lens;
+    int B, Lq, Lk, H_q, H_kv, D;
+    long long q_tstride, q_bstride, kv_tstride, kv_bstride;
+    float scale;
+    int grad_bf16;
+    void *dq, *dk, *dv;
+    float* workspace;  // Delta [B][H_q][Lq], then (bf16 gradients) dQ in fp32
+    cudaStream_t stream;
+};
+cudaError_t launch_cross_bwd(const CrossBwdArgs& a, unsigned long long wait_limit_ns,
+                             int deterministic, const char** why);
 cudaError_t read_and_clear_kv_error(unsigned int* value);
 
 }  // namespace ra

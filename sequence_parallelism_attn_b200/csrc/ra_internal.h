@@ -60,6 +60,11 @@ struct AttnBwdArgs {
     const int* pid = nullptr;     // packed samples: position_ids [B][P*Lc] (causal), else null
     int accumulate = 0;           // add into dq, dk, dv instead of overwriting them
     int deterministic = 0;        // dq from the query-stationary kernel (fixed order)
+    // cross attention (cross_Lq > 0): Lq query rows against Lc keys, P = 1, not causal
+    int cross_Lq = 0;
+    const int* kv_lens = nullptr;  // [B] keys per batch row (null: Lc)
+    long long q_tstride = 0, kv_tstride = 0;  // elements between tokens (0: dense)
+    int grad_bf16 = 0;             // dk, dv are bf16 (dq stays fp32)
     cudaStream_t stream;
 };
 
@@ -203,6 +208,9 @@ cudaError_t launch_attn_bwd_sm100(const AttnBwdArgs& a, unsigned long long wait_
                                   const char** why);
 cudaError_t read_and_clear_bwd_error(unsigned int* value);
 
+// The process-wide settings of ra_set_wait_limit_ns and ra_set_bwd_deterministic.
+unsigned long long wait_limit_ns();
+int bwd_deterministic();
 // Records msg as the calling thread's ra_last_error() text and returns status (for entry
 // points defined outside api.cu).
 int set_last_error(int status, const std::string& msg);

@@ -27,6 +27,7 @@ EXPORTED = ("ra_ring_attn_fwd", "ra_ring_attn_fwd_zigzag", "ra_ring_attn_fwd_pac
             "ra_ulysses_seq2head_scatter", "ra_ulysses_head2seq_scatter",
             "ra_ulysses_replica_sum", "ra_paged_kv_append", "ra_prefix_attn_fwd",
             "ra_prefix_attn_workspace", "ra_cross_attn_fwd", "ra_cross_attn_workspace",
+            "ra_cross_attn_bwd", "ra_cross_attn_bwd_workspace",
             "ra_sync_status", "ra_last_error", "ra_set_wait_limit_ns",
             "ra_set_bwd_deterministic", "ra_debug_inject_stall", "ra_version")
 
@@ -78,7 +79,11 @@ def load() -> ctypes.CDLL:
                                       [f32, i32, i32, vp, vp, vp, i64, vp])
     lib.ra_prefix_attn_workspace.argtypes = [i32] * 9
     lib.ra_cross_attn_workspace.argtypes = [i32] * 6
-    for f in ("ra_prefix_attn_workspace", "ra_cross_attn_workspace"):
+    lib.ra_cross_attn_bwd.argtypes = ([vp] * 7 + [i32] * 6 + [i64] * 4 +
+                                      [f32, i32, i32, vp, vp, vp, vp, i64, vp])
+    lib.ra_cross_attn_bwd_workspace.argtypes = [i32] * 5
+    for f in ("ra_prefix_attn_workspace", "ra_cross_attn_workspace",
+              "ra_cross_attn_bwd_workspace"):
         getattr(lib, f).restype = i64
     lib.ra_sync_status.argtypes = [vp]
     for f in ("ra_ring_attn_fwd", "ra_ring_attn_fwd_zigzag", "ra_ring_attn_fwd_packed",
@@ -87,7 +92,8 @@ def load() -> ctypes.CDLL:
               "ra_ulysses_seq2head", "ra_ulysses_head2seq", "ra_ulysses_seq2head_grouped",
               "ra_ulysses_head2seq_grouped", "ra_ulysses_replica_sum", "ra_sync_status",
               "ra_ulysses_seq2head_scatter", "ra_ulysses_head2seq_scatter",
-              "ra_paged_kv_append", "ra_prefix_attn_fwd", "ra_cross_attn_fwd"):
+              "ra_paged_kv_append", "ra_prefix_attn_fwd", "ra_cross_attn_fwd",
+              "ra_cross_attn_bwd"):
         getattr(lib, f).restype = ctypes.c_int
     lib.ra_last_error.restype = ctypes.c_char_p
     lib.ra_version.restype = ctypes.c_char_p
@@ -671,3 +677,39 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb, scale, RA_BF16, _dt(out.dtype), out.data_ptr(),
         lse.data_ptr(), ws, ws_bytes, _stream(None)))
     return out, lse
+
+
+def cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                   lse: torch.Tensor, dout: torch.Tensor, kv_lens: torch.Tensor | None = None,
+                   scale: float | None = None, grad_dtype: torch.dtype = torch.float32,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of cross_attn_fwd (ra_cross_attn_bwd): q, k, v, kv_lens and scale as given to
+    it, out (bf16) and lse its results, dout [B, Lq, H_q, D] bf16.  Returns dq
+    [B, Lq, H_q, D], dk, dv [B, Lk, H_kv, D] in grad_dtype (fp32 or bf16), zero past
+    kv_lens[b]."""
+    ctx = _where(q, stream)
+    if ctx is not None:
+        with ctx:
+            return cross_attn_bwd(q, k, v, out, lse, dout, kv_lens, scale, grad_dtype, workspace)
+    dev = q.device
+    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v)
+    if kv_lens is not None:
+        _ints(kv_lens, "kv_lens", dev, (B,))
+    _dense(out, "out", dev, (B, Lq, H_q, D), torch.bfloat16)
+    _dense(dout, "dout", dev, (B, Lq, H_q, D), torch.bfloat16)
+    _dense(lse, "lse", dev, (B, H_q, Lq), torch.float32)
+    if scale is None:
+        scale = D ** -0.5
+    dq = torch.empty((B, Lq, H_q, D), dtype=grad_dtype, device=dev)
+    dk = torch.empty((B, Lk, H_kv, D), dtype=grad_dtype, device=dev)
+    dv = torch.empty_like(dk)
+    lib = load()
+    gd = _dt(grad_dtype)
+    ws, ws_bytes, keep = _workspace(lib.ra_cross_attn_bwd_workspace(B, Lq, H_q, D, gd), workspace,
+                                    dev)
+    _check(lib.ra_cross_attn_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if kv_lens is None else kv_lens.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), dout.data_ptr(), B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb,
+        scale, RA_BF16, gd, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws, ws_bytes,
+        _stream(None)))
+    return dq, dk, dv

@@ -105,3 +105,53 @@ def rotate(x, pos, inv_freq, interleaved):
     xa, xb = x[..., a].clone(), x[..., b].clone()
     x[..., a], x[..., b] = xa * c - xb * s, xb * c + xa * s
     return x
+
+
+def cross_backward(q, k, v, lens, do, scale):
+    """CPU tensors -> (dq, dk, dv) in fp64, and a bound of each element's error by the
+    kernel's roundings: P and dS are rounded to bf16 (u each) before their products with dO,
+    k and q; Delta = rowsum(dO * O) is taken from O rounded to bf16, an error of at most
+    u sum_d |dO O| that P weighs; scores and exponentials add 2^-12 of P (see above)."""
+    B, Lq, H, D = q.shape
+    Hk = k.shape[2]
+    g = H // Hk
+    grads = [torch.zeros(x.shape, dtype=torch.float64) for x in (q, k, v)]
+    bounds = [torch.zeros_like(x) for x in grads]
+    for b in range(B):
+        n = int(lens[b])
+        if n == 0:
+            continue
+        qq, dd = q[b].double().transpose(0, 1), do[b].double().transpose(0, 1)
+        kk = k[b, :n].double().repeat_interleave(g, 1).transpose(0, 1)
+        vv = v[b, :n].double().repeat_interleave(g, 1).transpose(0, 1)
+        p = torch.softmax((qq @ kk.mT) * scale, -1)
+        o = p @ vv
+        dp = dd @ vv.mT
+        delta = (dd * o).sum(-1, keepdim=True)
+        ds = p * (dp - delta)
+        e = 2.0 ** -12
+        ds_err = (U + e) * ds.abs() + p * U * (dd * o).abs().sum(-1, keepdim=True) \
+            + p * 2.0 ** -16 * (dd.abs() @ vv.abs().mT)
+        p_err = (U + e) * p
+
+        def group(x):  # sum over the query heads of a kv head
+            return x.view(Hk, g, n, D).sum(1).transpose(0, 1)
+
+        grads[0][b] = (ds @ kk * scale).transpose(0, 1)
+        bounds[0][b] = (ds_err @ kk.abs() * scale).transpose(0, 1)
+        grads[1][b, :n] = group(ds.mT @ qq * scale)
+        bounds[1][b, :n] = group(ds_err.mT @ qq.abs() * scale)
+        grads[2][b, :n] = group(p.mT @ dd)
+        bounds[2][b, :n] = group(p_err.mT @ dd.abs())
+    return grads, bounds
+
+
+def check_grads(got, ref, label=""):
+    for name, x, want, tol in zip(("dq", "dk", "dv"), got, *ref):
+        x0, x = x, x.detach().double().cpu()
+        assert torch.isfinite(x).all(), f"{label} {name}: non-finite"
+        if x0.dtype == torch.bfloat16:
+            tol = tol + U * (want.abs() + tol)
+        err = (x - want).abs()
+        assert (err <= tol + 1e-30).all(), \
+            f"{label} {name}: {float((err / (tol + 1e-30)).max()):.3f} of its bound"

@@ -110,3 +110,46 @@ def test_binding_refusals():
                 (q, k, torch.zeros(2, 7, 4, 64, **bf)[:, :, :2])):
         with pytest.raises(ValueError):
             ra._cross_strides(*bad)
+
+
+CROSS_BWD = dict(q=FAKE, k=FAKE, v=FAKE, lens=FAKE, o=FAKE, lse=FAKE, do=FAKE, B=2, Lq=3, Lk=50,
+                 hq=4, hkv=2, d=64, qt=256, qb=768, kt=128, kb=6400, scale=0.125, dt=0, gdt=0,
+                 dq=FAKE, dk=FAKE, dv=FAKE, ws=FAKE, wsb=1 << 40)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=0), 1), (dict(k=0), 1), (dict(v=FAKE + 8), 1), (dict(lens=FAKE + 2), 1),
+    (dict(o=0), 1), (dict(lse=0), 1), (dict(do=FAKE + 2), 1), (dict(dq=0), 1),
+    (dict(dk=FAKE + 4), 1), (dict(dv=0), 1), (dict(ws=0), 1), (dict(wsb=100), 1),
+    (dict(B=0), 1), (dict(Lq=0), 1), (dict(Lk=0), 1), (dict(hkv=3), 1), (dict(d=32), 2),
+    (dict(qt=8), 1), (dict(qb=8), 1), (dict(kt=8), 1), (dict(kb=8), 1), (dict(scale=0.0), 1),
+    (dict(dt=1), 2), (dict(gdt=2), 1),
+])
+def test_cross_backward_refusals(lib, kw, status):
+    assert call(lib, "ra_cross_attn_bwd", CROSS_BWD, kw) == status
+    assert lib.ra_last_error()
+
+
+def test_cross_backward_workspace(lib):
+    # Delta rows, and dQ in fp32 where the gradients are rounded to bf16
+    assert lib.ra_cross_attn_bwd_workspace(2, 3, 4, 64, 1) == 4 * 24
+    assert lib.ra_cross_attn_bwd_workspace(2, 3, 4, 64, 0) == 4 * 24 * 65
+
+
+def test_reference_gradients_against_differences():
+    """The 64-bit formula that the GPU's gradients are held to is the derivative of the
+    64-bit forward, masked batch rows and grouped heads included."""
+    import _kv_ref as ref
+    g = torch.Generator().manual_seed(0)
+    q, k, v, do = (torch.randn(2, n, h, 8, generator=g, dtype=torch.float64)
+                   for n, h in ((3, 4), (5, 2), (5, 2), (3, 4)))
+    lens = [5, 3]
+    grads, _ = ref.cross_backward(q, k, v, lens, do, 0.3)
+    for i in range(3):
+        for at in [(0, 0, 0, 0), (1, 2, 1, 5), (0, 1, 1, 3)]:
+            def loss(h):
+                y = [t.clone() for t in (q, k, v)]
+                y[i][at] += h
+                return (ref.cross_attention(*y, lens, 0.3)[0] * do).sum()
+            d = (loss(1e-5) - loss(-1e-5)) / 2e-5
+            assert abs(d - grads[i][at]) <= 1e-8 * (1 + abs(d))
