@@ -378,19 +378,20 @@ ra_status ra_sync_status(void* stream) {
     e = ra::read_and_clear_error_word(&word);
     if (e == cudaSuccess) e = ra::read_and_clear_permute_error(&pword);
     if (e == cudaSuccess) e = ra::read_and_clear_bwd_error(&bword);
-    unsigned int kword = 0, aword = 0;
+    unsigned int kword = 0, aword = 0, tword = 0;
     if (e == cudaSuccess) e = ra::read_and_clear_kv_error(&kword);
+    if (e == cudaSuccess) e = ra::read_and_clear_kv_tile_error(&tword);
     if (e == cudaSuccess) e = ra::read_and_clear_append_error(&aword);
     if (e != cudaSuccess) return cuda_fail(e, "reading the kernel error word");
-    word |= (pword ? 16u : 0u) | (bword ? 64u : 0u);
+    word |= (pword ? 16u : 0u) | (bword ? 64u : 0u) | ((tword & 255u) ? 128u : 0u);
     if (word) {
-        char buf[128];
+        char buf[160];
         std::snprintf(buf, sizeof buf,
                       "a kernel gave up on a bounded wait (error bits 0x%x: 1 load, 2 mma, "
-                      "4 softmax, 8 drain, 16 permute, 64 backward)", word);
+                      "4 softmax, 8 drain, 16 permute, 64 backward, 128 cache tiles)", word);
         return fail(RA_ERR_TIMEOUT, buf);
     }
-    kword |= aword;
+    kword |= aword | (tword >> 8);
     if (kword) {
         char buf[160];
         std::snprintf(buf, sizeof buf,

@@ -155,7 +155,8 @@ long long ra_prefix_attn_workspace(int B, int n_tokens, int max_tokens, int max_
     if (B < 1 || n_tokens < 1 || max_tokens < 1 || max_len < 1 || prefix_len < 0 || H_kv < 1 ||
         H_q < 1 || H_q % H_kv != 0 || D < 1 || page_size < 1)
         return 0;
-    return ra::plan_kv_rows(B, n_tokens, max_tokens, max_len, prefix_len, H_q, H_kv, D).workspace;
+    return ra::plan_kv(B, n_tokens, max_tokens, max_len, prefix_len, H_q, H_kv, D, 1, page_size)
+        .workspace;
 }
 
 ra_status ra_prefix_attn_fwd(const void* q, long long q_tstride, const void* k_pages,
@@ -209,19 +210,20 @@ ra_status ra_prefix_attn_fwd(const void* q, long long q_tstride, const void* k_p
     a.workspace = workspace;
     a.stream = (cudaStream_t)stream;
     const ra::KvPlan plan =
-        ra::plan_kv_rows(B, n_tokens, max_tokens, max_len, prefix_len, H_q, H_kv, D);
+        ra::plan_kv(B, n_tokens, max_tokens, max_len, prefix_len, H_q, H_kv, D, 1, page_size);
     RA_CHECK(check_workspace(workspace, workspace_bytes, plan.workspace));
     if ((long long)n_tokens * H_q > 0x7fffffffLL || plan.blocks > 0x7fffffffLL)
         return fail(RA_ERR_INVALID, "problem too large for one launch");
-    const cudaError_t e = ra::launch_kv_rows(a, plan);
-    return e == cudaSuccess ? RA_OK : cuda_fail(e, "prefix attention launch");
+    const char* why = "prefix attention launch";
+    const cudaError_t e = ra::launch_kv(a, plan, ra::wait_limit_ns(), &why);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, why);
 }
 
 long long ra_cross_attn_workspace(int B, int Lq, int Lk, int H_q, int H_kv, int D) {
     if (B < 1 || Lq < 1 || Lk < 1 || H_kv < 1 || H_q < 1 || H_q % H_kv != 0 || D < 1 ||
         (long long)B * Lq > kMaxTokens)
         return 0;
-    return ra::plan_kv_rows(B, B * Lq, Lq, Lk, 0, H_q, H_kv, D).workspace;
+    return ra::plan_kv(B, B * Lq, Lq, Lk, 0, H_q, H_kv, D, 0, Lk).workspace;
 }
 
 // The sizes and strides that cross attention's forward and backward share.
@@ -283,12 +285,13 @@ ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v, const i
     a.lse = lse;
     a.workspace = workspace;
     a.stream = (cudaStream_t)stream;
-    const ra::KvPlan plan = ra::plan_kv_rows(B, B * Lq, Lq, Lk, 0, H_q, H_kv, D);
+    const ra::KvPlan plan = ra::plan_kv(B, B * Lq, Lq, Lk, 0, H_q, H_kv, D, 0, Lk);
     RA_CHECK(check_workspace(workspace, workspace_bytes, plan.workspace));
     if (plan.blocks > 0x7fffffffLL)
         return fail(RA_ERR_INVALID, "problem too large for one launch");
-    const cudaError_t e = ra::launch_kv_rows(a, plan);
-    return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross attention launch");
+    const char* why = "cross attention launch";
+    const cudaError_t e = ra::launch_kv(a, plan, ra::wait_limit_ns(), &why);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, why);
 }
 
 long long ra_cross_attn_bwd_workspace(int B, int Lq, int H_q, int D, ra_dtype grad_dtype) {

@@ -49,18 +49,26 @@ struct KvArgs {
     cudaStream_t stream;
 };
 
-// How a call is split: partial results of row (token, head) for every key range, joined by
-// the combine kernel.
+// How a call is split.  The prefix and the sequences' own keys are each taken by one of two
+// kernels, in ranges of `chunk` keys; every range of a row is a partial result (two where the
+// tile kernel's warpgroups share a row tile), which the combine kernel joins.
+constexpr int kKvNone = 0, kKvRows = 1, kKvTiles = 2;
 struct KvPlan {
-    int chunk_p, splits_p, tiles_p;  // prefix: keys per split, splits, row tiles
-    int chunk_o, splits_o, tiles_o;  // each sequence's own keys
-    int mt;                          // 16-row tiles per block
-    int direct;                      // one split in all: results written without partials
-    long long blocks, workspace;     // grid size, bytes
+    int kind_p, chunk_p, splits_p, tiles_p, ksplit_p, parts_p;  // the prefix
+    int kind_o, chunk_o, splits_o, tiles_o, ksplit_o, parts_o;  // own keys
+    int mt;                       // rows kernel: 16-row tiles per block
+    int direct;                   // a single part: results written without partials
+    long long blocks, workspace;  // blocks of the larger launch, bytes
 };
-KvPlan plan_kv_rows(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
-                    int H_kv, int D);
-cudaError_t launch_kv_rows(const KvArgs& a, const KvPlan& p);
+// paged: keys in pages of page_size (else dense batch rows).
+KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
+               int H_kv, int D, int paged, int page_size);
+// Everything of a plan: the tile kernel's part, the rows kernel's, the combine.
+cudaError_t launch_kv(const KvArgs& a, const KvPlan& p, unsigned long long wait_limit_ns,
+                      const char** why);
+cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& p, unsigned long long wait_limit_ns,
+                            const char** why);
+cudaError_t read_and_clear_kv_tile_error(unsigned int* value);
 
 struct CrossBwdArgs {
     const void *q, *k, *v, *out, *dout;

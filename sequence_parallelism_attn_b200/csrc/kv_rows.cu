@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_rows_kernel(const __grid_co
         }
         chunk = p.p.chunk_o;
         table = a.tables ? a.tables + (long long)b * a.max_pages : nullptr;
-        part = p.p.splits_p + split;
+        part = p.p.parts_p + split;
     }
     const int n_rows = n_tok * p.group;
     const int row0 = tile * C::ROWS;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
     if (row >= rows) return;
     const int tok = (int)(row / a.H_q), head = (int)(row - (long long)tok * a.H_q);
     if (a.cu && tok >= a.cu[a.B]) return;  // rows behind the last sequence stay as they were
-    const int ns = p.p.splits_p + p.p.splits_o;
+    const int ns = p.p.parts_p + p.p.parts_o;
     float mm = -INFINITY;
     for (int s = lane; s < ns; s += 32) mm = fmaxf(mm, p.part_lse[s * rows + row]);
 #pragma unroll
@@ -506,31 +506,87 @@ int chunk_for(long long blocks_per_split, int keys, long long target) {
 
 }  // namespace
 
-KvPlan plan_kv_rows(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
-                    int H_kv, int D) {
+namespace {
+
+// The tile kernel's share of a plan over `units` (batch rows) x H_kv heads, `tokens` tokens
+// and `keys` keys each: row blocks, and the number of key ranges that takes the least time
+// by a plain model (a wave of 148 blocks costs a range's key tiles and three more for
+// filling and draining; partials are written and read at 5 TB/s).
+void plan_tiles(long long units, int H_kv, int group, int tokens, int keys, int D,
+                long long part_bytes, bool joined, int& chunk, int& splits, int& blocks,
+                int& ksplit, int& parts) {
+    const int tpt = 128 / group, tiles = ceil_div(tokens, tpt);
+    ksplit = tiles == 1;
+    blocks = ksplit ? 1 : ceil_div(tiles, 2);
+    const int kt = ceil_div(keys, 128);
+    const double tile_us = (D == 128 ? 2.2 : 1.5) * (ksplit ? 0.6 : 1.0);
+    double best = 0;
+    splits = 0;
+    for (int s = 1; s <= kt && s <= 512; ++s) {
+        const int per = ceil_div(kt, s);
+        if (s > 1 && ceil_div(kt, per) != s) continue;  // the same ranges as fewer splits
+        const double waves = (double)ceil_div(units * H_kv * blocks * s, kSms);
+        const int np = s * (1 + ksplit);
+        const double join = np > 1 || joined ? 2.0 * np * part_bytes / 5e6 : 0.0;
+        const double us = waves * (per + 3) * tile_us + join + (np > 1 && !joined ? 3.0 : 0.0);
+        if (splits == 0 || us < best) {
+            best = us;
+            splits = s;
+        }
+    }
+    chunk = ceil_div(kt, splits) * 128;
+    parts = splits * (1 + ksplit);
+}
+
+}  // namespace
+
+KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
+               int H_kv, int D, int paged, int page_size) {
     KvPlan p = {};
     const int group = H_q / H_kv;
     const long long rows_o = (long long)max_tokens * group, rows_p = (long long)n_tokens * group;
-    const long long most = prefix_len > 0 && rows_p > rows_o ? rows_p : rows_o;
-    p.mt = most > 16 ? 2 : 1;
+    // the tile kernel takes whole groups of heads, and pages that divide its 128-key tiles
+    const bool tiles_ok =
+        group <= 128 && (!paged || (page_size >= 8 && (page_size & (page_size - 1)) == 0));
+    const long long part_bytes = (long long)n_tokens * H_q * (D + 1) * 4;
+    p.kind_p = prefix_len == 0 ? kKvNone : (tiles_ok && rows_p > 32 ? kKvTiles : kKvRows);
+    p.kind_o = tiles_ok && rows_o > 32 ? kKvTiles : kKvRows;
+    const long long rows_most = p.kind_p == kKvRows && rows_p > rows_o ? rows_p
+                                : p.kind_o == kKvRows                  ? rows_o
+                                                                       : rows_p;
+    p.mt = rows_most > 16 ? 2 : 1;
     const int R = 16 * p.mt;
-    p.tiles_o = ceil_div(rows_o, R);
-    p.chunk_o = chunk_for((long long)B * H_kv * p.tiles_o, max_len, 8LL * kSms);
-    p.splits_o = max_len > 0 ? ceil_div(max_len, p.chunk_o) : 1;
-    if (prefix_len > 0) {
+    if (p.kind_p == kKvRows) {
         p.tiles_p = ceil_div(rows_p, R);
         p.chunk_p = chunk_for((long long)H_kv * p.tiles_p, prefix_len, 4LL * kSms);
-        p.splits_p = ceil_div(prefix_len, p.chunk_p);
+        p.splits_p = p.parts_p = ceil_div(prefix_len, p.chunk_p);
+    } else if (p.kind_p == kKvTiles) {
+        plan_tiles(1, H_kv, group, n_tokens, prefix_len, D, part_bytes, true, p.chunk_p,
+                   p.splits_p, p.tiles_p, p.ksplit_p, p.parts_p);
     }
-    p.direct = p.splits_p + p.splits_o == 1;
-    p.blocks = (long long)p.splits_p * H_kv * p.tiles_p +
-               (long long)B * p.splits_o * H_kv * p.tiles_o;
-    p.workspace = p.direct ? 0
-                           : (long long)(p.splits_p + p.splits_o) * n_tokens * H_q * (D + 1) * 4;
+    if (p.kind_o == kKvRows) {
+        p.tiles_o = ceil_div(rows_o, R);
+        p.chunk_o = chunk_for((long long)B * H_kv * p.tiles_o, max_len, 8LL * kSms);
+        p.splits_o = p.parts_o = ceil_div(max_len, p.chunk_o);
+    } else {
+        plan_tiles(B, H_kv, group, max_tokens, max_len, D, part_bytes, p.kind_p != kKvNone,
+                   p.chunk_o, p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
+    }
+    p.direct = p.parts_p + p.parts_o == 1;
+    const long long bp = (long long)p.splits_p * H_kv * p.tiles_p,
+                    bo = (long long)B * p.splits_o * H_kv * p.tiles_o;
+    p.blocks = bp + bo;
+    p.workspace = p.direct ? 0 : (p.parts_p + p.parts_o) * part_bytes;
     return p;
 }
 
-cudaError_t launch_kv_rows(const KvArgs& a, const KvPlan& plan) {
+cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wait_limit_ns,
+                      const char** why) {
+    cudaError_t e = cudaSuccess;
+    if (plan.kind_p == kKvTiles || plan.kind_o == kKvTiles) {
+        e = launch_kv_tiles(a, plan, wait_limit_ns, why);
+        if (e != cudaSuccess) return e;
+    }
     RowsParams p;
     p.a = a;
     p.p = plan;
@@ -538,17 +594,27 @@ cudaError_t launch_kv_rows(const KvArgs& a, const KvPlan& plan) {
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     const long long rows = (long long)a.n_tokens * a.H_q;
     p.part_o = (float*)a.workspace;
-    p.part_lse = p.part_o + (long long)(plan.splits_p + plan.splits_o) * rows * a.D;
-    p.items_p = (unsigned)((long long)plan.splits_p * a.H_kv * plan.tiles_p);
-    const bool page16 = !a.tables || a.page_size % kKeys == 0;
-    cudaError_t e;
-    const unsigned gr = (unsigned)plan.blocks;
-    if (a.D == 128) {
-        if (plan.mt == 1) e = page16 ? launch_rows<128, 1, true>(p, gr) : launch_rows<128, 1, false>(p, gr);
-        else e = page16 ? launch_rows<128, 2, true>(p, gr) : launch_rows<128, 2, false>(p, gr);
-    } else {
-        if (plan.mt == 1) e = page16 ? launch_rows<64, 1, true>(p, gr) : launch_rows<64, 1, false>(p, gr);
-        else e = page16 ? launch_rows<64, 2, true>(p, gr) : launch_rows<64, 2, false>(p, gr);
+    p.part_lse = p.part_o + (long long)(plan.parts_p + plan.parts_o) * rows * a.D;
+    p.items_p = plan.kind_p == kKvRows
+                    ? (unsigned)((long long)plan.splits_p * a.H_kv * plan.tiles_p)
+                    : 0;
+    const unsigned grid =
+        p.items_p + (plan.kind_o == kKvRows
+                         ? (unsigned)((long long)a.B * plan.splits_o * a.H_kv * plan.tiles_o)
+                         : 0);
+    if (grid > 0) {
+        const bool page16 = !a.tables || a.page_size % kKeys == 0;
+        if (a.D == 128) {
+            if (plan.mt == 1)
+                e = page16 ? launch_rows<128, 1, true>(p, grid) : launch_rows<128, 1, false>(p, grid);
+            else
+                e = page16 ? launch_rows<128, 2, true>(p, grid) : launch_rows<128, 2, false>(p, grid);
+        } else {
+            if (plan.mt == 1)
+                e = page16 ? launch_rows<64, 1, true>(p, grid) : launch_rows<64, 1, false>(p, grid);
+            else
+                e = page16 ? launch_rows<64, 2, true>(p, grid) : launch_rows<64, 2, false>(p, grid);
+        }
     }
     if (e != cudaSuccess || plan.direct) return e;
     const unsigned cg = (unsigned)((rows + 3) / 4);

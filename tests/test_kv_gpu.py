@@ -72,6 +72,13 @@ PREFIX = [  # n, lens, page, hq, hkv, d, prefix
     ([2], [2], 256, 8, 8, 128, 3000),
     ([65, 130], [65, 200], 64, 8, 2, 128, 300),
     ([33], [400], 8, 4, 1, 64, 129),
+    ([20], [20], 32, 4, 1, 64, 2111),                         # one row tile, odd key tiles
+    ([50], [50], 16, 4, 1, 128, 1500),
+    ([64, 64], [64, 700], 256, 2, 2, 128, 640),
+    ([5, 60], [1, 61], 8, 16, 1, 64, 9),                      # more new tokens than own keys
+    ([140], [141], 128, 1, 1, 128, 127),
+    ([3, 2], [30, 9], 16, 48, 1, 64, 50),                     # 48 heads per kv head
+    ([2, 1], [30, 9], 16, 130, 1, 64, 50),                    # more than a row tile's
 ]
 
 
@@ -282,6 +289,9 @@ CROSS = [  # B, Lq, Lk, lens, hq, hkv, d
     (1, 130, 77, [70], 8, 8, 64),
     (2, 300, 129, [129, 128], 2, 2, 128),
     (3, 257, 640, [1, 0, 513], 7, 1, 64),
+    (1, 40, 1100, [1029], 1, 1, 128),
+    (2, 500, 64, [64, 63], 8, 2, 64),
+    (1, 129, 2000, None, 2, 1, 64),
 ]
 
 
