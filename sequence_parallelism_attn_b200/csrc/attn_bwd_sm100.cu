@@ -1515,6 +1515,8 @@ cudaError_t launch_bwd_d(const BwdParams& p, const AttnBwdArgs& a, const char** 
 cudaError_t launch_attn_bwd_sm100(const AttnBwdArgs& a, unsigned long long wait_limit_ns,
                                   const char** why) {
     static thread_local BwdParams p;
+    const cudaError_t ctx = ensure_context();
+    if (ctx != cudaSuccess) return ctx;
     const long long L = a.cross_Lq ? a.cross_Lq : (long long)a.P * a.Lc;
     if (!bwd_tile_map(&p.tm_q, a.q, a.D, a.H_q, L, a.B, a.q_bstride, a.q_tstride) ||
         !bwd_tile_map(&p.tm_do, a.dout, a.D, a.H_q, L, a.B, L * a.H_q * a.D)) {

@@ -724,6 +724,8 @@ cudaError_t launch_d(const AttnParams& p, int grid, cudaStream_t stream, const c
 cudaError_t launch_attn_sm100(const AttnArgs& a, unsigned long long wait_limit_ns,
                               int inject_stall, const char** why) {
     static thread_local AttnParams p;  // ~16.6 KB of tensor maps: kept off the stack
+    const cudaError_t ctx = ensure_context();
+    if (ctx != cudaSuccess) return ctx;
     const long long L = (long long)a.P * a.Lc;
     if (!encode_tile_map(&p.tm_q, a.q, a.D, a.H_q, L, a.B, a.q_bstride)) {
         *why = "cuTensorMapEncodeTiled failed for q";

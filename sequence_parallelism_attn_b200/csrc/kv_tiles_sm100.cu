@@ -688,6 +688,8 @@ cudaError_t launch(const TileParams& p, unsigned grid, const char** why) {
 
 cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& plan, unsigned long long wait_limit_ns,
                             const char** why) {
+    const cudaError_t ctx = ensure_context();
+    if (ctx != cudaSuccess) return ctx;
     TileParams p;
     p.a = a;
     p.group = a.H_q / a.H_kv;

@@ -183,6 +183,16 @@ __host__ __device__ inline int key_tile_q_ranges(int layout, int P, int Lc, int 
     return nr;
 }
 
+// Makes the current device's primary context current on this thread.  The runtime calls of
+// a launch do that by themselves, but cuTensorMapEncodeTiled, a driver call, fails with an
+// invalid context on a thread whose first CUDA call it is (autograd's backward thread, when
+// every allocation comes from torch's cache).  Free of synchronisation; legal in a capture.
+inline cudaError_t ensure_context() {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e == cudaSuccess ? cudaSetDevice(dev) : e;
+}
+
 // Tensor-core (tcgen05) attention for bf16 inputs, D in {64, 128}.
 cudaError_t launch_attn_sm100(const AttnArgs& a, unsigned long long wait_limit_ns,
                               int inject_stall, const char** why);
