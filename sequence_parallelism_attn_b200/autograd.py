@@ -133,9 +133,8 @@ class _CrossAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do):
         q, k, v, o, lse, kv_lens = ctx.saved_tensors
-        dq, dk, dv = ra.cross_attn_bwd(q, k, v, o, lse, do.to(q.dtype).contiguous(), kv_lens,
-                                       ctx.scale, grad_dtype=q.dtype)
-        return dq, dk, dv, None, None
+        return (*ra.cross_attn_bwd(q, k, v, o, lse, do.contiguous(), kv_lens, ctx.scale,
+                                   grad_dtype=q.dtype), None, None)
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

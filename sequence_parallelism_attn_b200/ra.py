@@ -8,6 +8,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -441,59 +442,68 @@ def ring_attn_fwd(q: torch.Tensor, k_chunks, v_chunks, causal: bool, scale: floa
 
 
 # ------------------------------------------------------------------ attention over a K/V cache
+# These helpers run once per decoded token, so their checks ask a tensor for as little as
+# possible: one shape, one stride tuple, the device's index.
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _where(t: torch.Tensor, stream):
     """Context in which a call on t's device allocates and launches: t's device where it is
     not the current one, and the stream that was given (so that what is allocated here
-    belongs to the stream that uses it)."""
+    belongs to the stream that uses it); None where the current ones are right."""
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
                                                device=t.device)
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
+    if not t.is_cuda:
+        raise ValueError("the tensors must be on a CUDA device")
+    if t.get_device() != torch.cuda.current_device():
         return torch.cuda.device(t.device)
     return None
 
 
-def _rows(t: torch.Tensor, name: str, device) -> None:
-    """A tensor of token rows [..., H, D] whose heads are dense."""
-    H, D = t.shape[-2:]
-    if t.device != device or t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be a bf16 tensor on {device}")
-    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D):
+def _raw_stream(device: int) -> int:
+    """The current stream of a device (what torch.cuda.current_stream wraps)."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _rows(t: torch.Tensor, name: str, device: int):
+    """Shape and strides of token rows [..., H, D] whose heads are dense, on device (-1: CPU)."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != _bf16 or t.get_device() != device:
+        raise ValueError(f"{name} must be a bf16 tensor on device {device}")
+    if stride[-1] != 1 or (stride[-2] != shape[-1] and shape[-2] > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
+    return shape, stride
 
 
-def _ints(t: torch.Tensor, name: str, device, shape) -> None:
-    if t.device != device or t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-    if tuple(t.shape) != shape:
+def _ints(t: torch.Tensor, name: str, device: int, shape) -> None:
+    if t.dtype != _i32 or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on device {device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
 
 
-def _dense(t: torch.Tensor, name: str, device, shape, dtype) -> None:
-    if t.device != device or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+def _dense(t: torch.Tensor, name: str, device: int, shape, dtype) -> None:
+    if t.dtype != dtype or t.get_device() != device or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on device "
+                         f"{device}")
 
 
-def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, device):
+def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, device: int):
     """(n_pages, page_size, H_kv, D, page stride) of a cache [n_pages, page_size, H_kv, D]."""
-    if k_pages.shape != v_pages.shape or k_pages.dim() != 4:
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must both be [n_pages, page_size, H_kv, D]")
-    n_pages, page_size, H_kv, D = k_pages.shape
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _rows(t, name, device)
-        if page_size > 1 and t.stride(1) != H_kv * D:
-            raise ValueError(f"{name}: the rows of a page must be dense")
-    stride = k_pages.stride(0) if n_pages > 1 else page_size * H_kv * D
-    if n_pages > 1 and v_pages.stride(0) != stride:
+    (n_pages, page_size, H_kv, D), ks = _rows(k_pages, "k_pages", device)
+    _, vs = _rows(v_pages, "v_pages", device)
+    if page_size > 1 and (ks[1] != H_kv * D or vs[1] != H_kv * D):
+        raise ValueError("the rows of a page must be dense")
+    if n_pages == 1:
+        return n_pages, page_size, H_kv, D, page_size * H_kv * D
+    if ks[0] != vs[0]:
         raise ValueError("k_pages and v_pages must have the same page stride")
-    return n_pages, page_size, H_kv, D, stride
-
-
-def _tstride(t: torch.Tensor, dim: int) -> int:
-    """Elements between tokens; the dense value where there is a single one."""
-    return t.stride(dim) if t.shape[dim] > 1 else t.shape[-2] * t.shape[-1]
+    return n_pages, page_size, H_kv, D, ks[0]
 
 
 def paged_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -512,53 +522,81 @@ def paged_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
         with ctx:
             return paged_kv_append(q, k, v, k_pages, v_pages, cu_tokens, seq_lens, block_tables,
                                    inv_freq, max_tokens, pos_offset, interleaved, q_out)
-    dev = k.device
+    dev = k.get_device()
     n_pages, page_size, H_kv, D, page_stride = _cache(k_pages, v_pages, dev)
-    N = k.shape[0]
-    if tuple(k.shape) != (N, H_kv, D) or v.shape != k.shape:
+    shape, ks = _rows(k, "k", dev)
+    N = shape[0]
+    if shape != (N, H_kv, D) or v.shape != shape:
         raise ValueError("k and v must be [N, H_kv, D] with the cache's heads")
-    _rows(k, "k", dev)
-    _rows(v, "v", dev)
+    _, vs = _rows(v, "v", dev)
     B, max_pages = block_tables.shape
     _ints(cu_tokens, "cu_tokens", dev, (B + 1,))
     _ints(seq_lens, "seq_lens", dev, (B,))
     _ints(block_tables, "block_tables", dev, (B, max_pages))
-    rot = 0
+    rot, inv_ptr = 0, None
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _dense(inv_freq, "inv_freq", dev, (rot // 2,), torch.float32)
+        _dense(inv_freq, "inv_freq", dev, (rot // 2,), _f32)
+        inv_ptr = inv_freq.data_ptr()
     H_q = q_ptr = q_ts = qo_ptr = qo_ts = 0
     if q is not None:
-        H_q = q.shape[1]
-        if tuple(q.shape) != (N, H_q, D):
+        shape, qs = _rows(q, "q", dev)
+        H_q = shape[1]
+        if shape != (N, H_q, D):
             raise ValueError("q must be [N, H_q, D]")
-        _rows(q, "q", dev)
+        dense = H_q * D
+        q_ptr, q_ts, qo_ts = q.data_ptr(), qs[0] if N > 1 else dense, dense
         if q_out is None:
-            q_out = torch.empty((N, H_q, D), dtype=torch.bfloat16, device=dev)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
+            q_out = q.new_empty(shape)
         else:
-            _rows(q_out, "q_out", dev)
-        q_ptr, q_ts, qo_ptr, qo_ts = (q.data_ptr(), _tstride(q, 0), q_out.data_ptr(),
-                                      _tstride(q_out, 0))
-    _check(load().ra_paged_kv_append(
-        q_ptr, k.data_ptr(), v.data_ptr(), q_ts, _tstride(k, 0), _tstride(v, 0),
-        cu_tokens.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(),
-        inv_freq.data_ptr() if rot else None, B, N, min(max_tokens, N), H_q, H_kv, D, rot,
-        int(interleaved), pos_offset, page_size, n_pages, max_pages, page_stride, RA_BF16, qo_ptr,
-        qo_ts, k_pages.data_ptr(), v_pages.data_ptr(), _stream(None)))
+            got, os = _rows(q_out, "q_out", dev)
+            if got != shape:
+                raise ValueError("q_out must have q's shape")
+            if N > 1:
+                qo_ts = os[0]
+        qo_ptr = q_out.data_ptr()
+    dense = H_kv * D
+    _check((_lib or load()).ra_paged_kv_append(
+        q_ptr, k.data_ptr(), v.data_ptr(), q_ts, ks[0] if N > 1 else dense,
+        vs[0] if N > 1 else dense, cu_tokens.data_ptr(), seq_lens.data_ptr(),
+        block_tables.data_ptr(), inv_ptr, B, N, max_tokens if max_tokens < N else N, H_q, H_kv, D,
+        rot, 1 if interleaved else 0, pos_offset, page_size, n_pages, max_pages, page_stride,
+        RA_BF16, qo_ptr, qo_ts, k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev)))
     return q_out if q is not None else None
 
 
-def _workspace(need: int, workspace: torch.Tensor | None, dev):
-    """(pointer, bytes) of the caller's workspace, or of a new one, and the tensor itself."""
+@functools.lru_cache(maxsize=4096)
+def _prefix_workspace(*sizes: int) -> int:
+    return load().ra_prefix_attn_workspace(*sizes)
+
+
+@functools.lru_cache(maxsize=4096)
+def _cross_workspace(*sizes: int) -> int:
+    return load().ra_cross_attn_workspace(*sizes)
+
+
+def _workspace(need: int, workspace: torch.Tensor | None, like: torch.Tensor, device: int):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        workspace = like.new_empty((need + 1) // 2)  # bf16 elements
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _results(q: torch.Tensor, shape, lse_shape, out_dtype, out, lse, device: int):
+    """The outputs that were given, checked, or new ones."""
+    if out is None:
+        out = q.new_empty(shape, dtype=out_dtype)
+    else:
+        _dense(out, "out", device, shape, out.dtype)
+    if lse is None:
+        lse = q.new_empty(lse_shape, dtype=_f32)
+    else:
+        _dense(lse, "lse", device, lse_shape, _f32)
+    return out, lse, _dt(out.dtype)
 
 
 def prefix_attn_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -582,12 +620,12 @@ def prefix_attn_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
             return prefix_attn_fwd(q, k_pages, v_pages, cu_tokens, seq_lens, block_tables,
                                    max_tokens, max_len, prefix_table, prefix_len, scale,
                                    out_dtype, out, lse, workspace)
-    dev = q.device
+    dev = q.get_device()
     n_pages, page_size, H_kv, D, page_stride = _cache(k_pages, v_pages, dev)
-    N, H_q, Dq = q.shape
+    shape, qs = _rows(q, "q", dev)
+    N, H_q, Dq = shape
     if Dq != D:
         raise ValueError("q and the cache must have the same head dimension")
-    _rows(q, "q", dev)
     B, max_pages = block_tables.shape
     _ints(cu_tokens, "cu_tokens", dev, (B + 1,))
     _ints(seq_lens, "seq_lens", dev, (B,))
@@ -600,44 +638,35 @@ def prefix_attn_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         table = prefix_table.data_ptr()
     if max_len is None:
         max_len = max_pages * page_size
-    max_tokens = min(max_tokens, N)
+    if max_tokens > N:
+        max_tokens = N
     if scale is None:
         scale = D ** -0.5
-    if out is None:
-        out = torch.empty((N, H_q, D), dtype=out_dtype, device=dev)
-    else:
-        _dense(out, "out", dev, (N, H_q, D), out.dtype)
-    if lse is None:
-        lse = torch.empty((H_q, N), dtype=torch.float32, device=dev)
-    else:
-        _dense(lse, "lse", dev, (H_q, N), torch.float32)
-    lib = load()
+    out, lse, out_dt = _results(q, shape, (H_q, N), out_dtype, out, lse, dev)
     ws, ws_bytes, keep = _workspace(
-        lib.ra_prefix_attn_workspace(B, N, max_tokens, max_len, prefix_len, H_q, H_kv, D,
-                                     page_size), workspace, dev)
-    _check(lib.ra_prefix_attn_fwd(
-        q.data_ptr(), _tstride(q, 0), k_pages.data_ptr(), v_pages.data_ptr(),
+        _prefix_workspace(B, N, max_tokens, max_len, prefix_len, H_q, H_kv, D, page_size),
+        workspace, q, dev)
+    _check((_lib or load()).ra_prefix_attn_fwd(
+        q.data_ptr(), qs[0] if N > 1 else H_q * D, k_pages.data_ptr(), v_pages.data_ptr(),
         cu_tokens.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(), table, prefix_len, B,
         N, max_tokens, max_len, H_q, H_kv, D, page_size, n_pages, max_pages, page_stride, scale,
-        RA_BF16, _dt(out.dtype), out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _stream(None)))
+        RA_BF16, out_dt, out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _raw_stream(dev)))
     return out, lse
 
 
-def _cross_strides(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
+def _cross_strides(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, device: int):
     """Checked sizes and strides of cross attention's inputs."""
-    dev = q.device
     if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
         raise ValueError("q must be [B, Lq, H_q, D], k and v [B, Lk, H_kv, D]")
-    B, Lq, H_q, D = q.shape
-    _, Lk, H_kv, _ = k.shape
-    if k.shape[0] != B or k.shape[3] != D:
+    (B, Lq, H_q, D), qs = _rows(q, "q", device)
+    (Bk, Lk, H_kv, Dk), ks = _rows(k, "k", device)
+    _, vs = _rows(v, "v", device)
+    if Bk != B or Dk != D:
         raise ValueError("q, k and v must have the same batch and head dimension")
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _rows(t, name, dev)
-    qt, kt = _tstride(q, 1), _tstride(k, 1)
-    qb = q.stride(0) if B > 1 else max(Lq * qt, Lq * H_q * D)
-    kb = k.stride(0) if B > 1 else max(Lk * kt, Lk * H_kv * D)
-    if (Lk > 1 and v.stride(1) != kt) or (B > 1 and v.stride(0) != kb):
+    # the stride of a dimension with one entry says nothing: the dense one in its place
+    qt, kt = (qs[1] if Lq > 1 else H_q * D), (ks[1] if Lk > 1 else H_kv * D)
+    qb, kb = (qs[0], ks[0]) if B > 1 else (Lq * qt, Lk * kt)
+    if (Lk > 1 and vs[1] != kt) or (B > 1 and vs[0] != kb):
         raise ValueError("k and v must have the same strides")
     return B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb
 
@@ -655,27 +684,19 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if ctx is not None:
         with ctx:
             return cross_attn_fwd(q, k, v, kv_lens, scale, out_dtype, out, lse, workspace)
-    dev = q.device
-    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v)
+    dev = q.get_device()
+    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v, dev)
+    lens = None
     if kv_lens is not None:
         _ints(kv_lens, "kv_lens", dev, (B,))
+        lens = kv_lens.data_ptr()
     if scale is None:
         scale = D ** -0.5
-    if out is None:
-        out = torch.empty((B, Lq, H_q, D), dtype=out_dtype, device=dev)
-    else:
-        _dense(out, "out", dev, (B, Lq, H_q, D), out.dtype)
-    if lse is None:
-        lse = torch.empty((B, H_q, Lq), dtype=torch.float32, device=dev)
-    else:
-        _dense(lse, "lse", dev, (B, H_q, Lq), torch.float32)
-    lib = load()
-    ws, ws_bytes, keep = _workspace(lib.ra_cross_attn_workspace(B, Lq, Lk, H_q, H_kv, D),
-                                    workspace, dev)
-    _check(lib.ra_cross_attn_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if kv_lens is None else kv_lens.data_ptr(),
-        B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb, scale, RA_BF16, _dt(out.dtype), out.data_ptr(),
-        lse.data_ptr(), ws, ws_bytes, _stream(None)))
+    out, lse, out_dt = _results(q, (B, Lq, H_q, D), (B, H_q, Lq), out_dtype, out, lse, dev)
+    ws, ws_bytes, keep = _workspace(_cross_workspace(B, Lq, Lk, H_q, H_kv, D), workspace, q, dev)
+    _check((_lib or load()).ra_cross_attn_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb,
+        scale, RA_BF16, out_dt, out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _raw_stream(dev)))
     return out, lse
 
 
@@ -691,25 +712,27 @@ def cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
     if ctx is not None:
         with ctx:
             return cross_attn_bwd(q, k, v, out, lse, dout, kv_lens, scale, grad_dtype, workspace)
-    dev = q.device
-    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v)
+    dev = q.get_device()
+    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v, dev)
+    lens = None
     if kv_lens is not None:
         _ints(kv_lens, "kv_lens", dev, (B,))
-    _dense(out, "out", dev, (B, Lq, H_q, D), torch.bfloat16)
-    _dense(dout, "dout", dev, (B, Lq, H_q, D), torch.bfloat16)
-    _dense(lse, "lse", dev, (B, H_q, Lq), torch.float32)
+        lens = kv_lens.data_ptr()
+    shape = (B, Lq, H_q, D)
+    _dense(out, "out", dev, shape, _bf16)
+    _dense(dout, "dout", dev, shape, _bf16)
+    _dense(lse, "lse", dev, (B, H_q, Lq), _f32)
     if scale is None:
         scale = D ** -0.5
-    dq = torch.empty((B, Lq, H_q, D), dtype=grad_dtype, device=dev)
-    dk = torch.empty((B, Lk, H_kv, D), dtype=grad_dtype, device=dev)
-    dv = torch.empty_like(dk)
-    lib = load()
+    dq = q.new_empty(shape, dtype=grad_dtype)
+    dk = q.new_empty((B, Lk, H_kv, D), dtype=grad_dtype)
+    dv = q.new_empty((B, Lk, H_kv, D), dtype=grad_dtype)
+    lib = _lib or load()
     gd = _dt(grad_dtype)
     ws, ws_bytes, keep = _workspace(lib.ra_cross_attn_bwd_workspace(B, Lq, H_q, D, gd), workspace,
-                                    dev)
+                                    q, dev)
     _check(lib.ra_cross_attn_bwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if kv_lens is None else kv_lens.data_ptr(),
-        out.data_ptr(), lse.data_ptr(), dout.data_ptr(), B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb,
-        scale, RA_BF16, gd, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws, ws_bytes,
-        _stream(None)))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, out.data_ptr(), lse.data_ptr(),
+        dout.data_ptr(), B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb, scale, RA_BF16, gd,
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws, ws_bytes, _raw_stream(dev)))
     return dq, dk, dv

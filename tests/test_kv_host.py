@@ -89,7 +89,7 @@ def test_binding_refusals():
     """The Python helpers check shapes, types and layouts before the library is called."""
     from sequence_parallelism_attn_b200 import ra
     bf = dict(dtype=torch.bfloat16)
-    dev = torch.device("cpu")
+    dev = -1  # the CPU
     pages = torch.zeros(4, 16, 2, 64, **bf)
     with pytest.raises(ValueError):
         ra._cache(pages, pages[:, :8], dev)
@@ -103,13 +103,15 @@ def test_binding_refusals():
         ra._ints(torch.zeros(3, dtype=torch.int64), "x", dev, (3,))
     with pytest.raises(ValueError):
         ra._ints(torch.zeros(3, dtype=torch.int32), "x", dev, (4,))
+    with pytest.raises(ValueError):
+        ra.cross_attn_fwd(*(torch.zeros(2, 5, 4, 64, **bf),) * 3)  # not on a GPU
     q, k = torch.zeros(2, 5, 4, 64, **bf), torch.zeros(2, 7, 2, 64, **bf)
-    assert ra._cross_strides(q, k, k) == (2, 5, 7, 4, 2, 64, 256, 1280, 128, 896)
+    assert ra._cross_strides(q, k, k, dev) == (2, 5, 7, 4, 2, 64, 256, 1280, 128, 896)
     for bad in ((q, k[:1], k[:1]), (q, k[..., :32], k[..., :32]), (q, k, k[:, :6]),
                 (q.float(), k, k), (q.transpose(1, 2), k, k),
                 (q, k, torch.zeros(2, 7, 4, 64, **bf)[:, :, :2])):
         with pytest.raises(ValueError):
-            ra._cross_strides(*bad)
+            ra._cross_strides(*bad, dev)
 
 
 CROSS_BWD = dict(q=FAKE, k=FAKE, v=FAKE, lens=FAKE, o=FAKE, lse=FAKE, do=FAKE, B=2, Lq=3, Lk=50,
