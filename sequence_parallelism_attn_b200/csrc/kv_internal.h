@@ -50,15 +50,18 @@ struct KvArgs {
 };
 
 // How a call is split.  The prefix and the sequences' own keys are each taken by one of two
-// kernels, in ranges of `chunk` keys; every range of a row is a partial result (two where the
-// tile kernel's warpgroups share a row tile), which the combine kernel joins.
+// kernels: the tile kernel in ranges of `chunk` keys, each a partial result of its rows (two
+// where its warpgroups share a row tile), or the rows kernel, whose warps share the keys out
+// evenly among themselves.  The combine kernel joins the partials.
 constexpr int kKvNone = 0, kKvRows = 1, kKvTiles = 2;
 struct KvPlan {
     int kind_p, chunk_p, splits_p, tiles_p, ksplit_p, parts_p;  // the prefix
     int kind_o, chunk_o, splits_o, tiles_o, ksplit_o, parts_o;  // own keys
-    int mt;                       // rows kernel: 16-row tiles per block
+    int mt;                       // rows kernel: 16-row fragments of a row tile
+    int row_blocks, j_own;        // its grid; index of the first (sequence, head, tile)
+    long long slots;              // its partial slots
     int direct;                   // a single part: results written without partials
-    long long blocks, workspace;  // blocks of the larger launch, bytes
+    long long blocks, workspace;  // largest index of a launch (to be below 2^31), bytes
 };
 // paged: keys in pages of page_size (else dense batch rows).
 KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,

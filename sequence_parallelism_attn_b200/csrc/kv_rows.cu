@@ -1,15 +1,20 @@
 // kv_rows.cu -- attention of few query rows over many keys: the single-token form of the
-// paged, prefix and cross attention.
+// paged, prefix and cross attention, and the joining of every form's partial results.
 //
-// A block takes 16 or 32 query rows (tokens x the query heads that share a kv head), one kv
-// head and one range of keys, either of the prefix that every sequence sees (rows of the
-// whole batch, so the prefix is read once) or of one sequence's own keys.  Its four warps
-// take the range's 16-key groups in turn, each warp with its own running softmax state
-// (maximum m, sum l, output O, all fp32) and its own ring of cp.async stages, so no warp
-// waits for another until the range is done; the four states are then merged by
-//   m* = max m_w,   O = sum 2^(m_w - m*) O_w / sum 2^(m_w - m*) l_w
-// and written as one partial result (O, log2-sum) of the rows, or as the final one where
-// the call has a single range.  The combine kernel merges a row's partials the same way.
+// Work is counted in 16-key groups of (sequence, kv head, row tile) -- row tiles of 16 or 32
+// rows, tokens x the query heads that share the kv head -- laid end to end: the prefix first
+// (rows of the whole batch, so its keys are read once), then every sequence's own keys.  The
+// resident warps (four to a block, two blocks to an SM) each take an equal stretch of that
+// line, whatever the sequences' lengths, and run it as one stream: a ring of cp.async
+// stages that is filled across the borders between heads and sequences, and a softmax state
+// (maximum m, sum l, output O, all fp32) that is written out as a partial result at each
+// border.  No warp waits for another.  A first form with a block per key range and a merge
+// of its four warps' states took 82 us where this takes less (12 sequences of 1001 .. 16384
+// keys, 8 kv heads of 128): its blocks spent some 4 us each on starting, filling and merging.
+//
+// Warp w's piece of the j-th (sequence, head, tile) is partial slot w + j (along the line
+// one of the two grows at every border, so no slot is used twice), and the pieces of one j
+// lie next to each other; the warp that has its first key notes where and how many.
 //
 // What bounds it: 16 rows need 4 D flops per key against 4 D bytes of K and V, far below the
 // machine's balance, so it runs at the rate at which K and V arrive.  Hence mma.sync on
@@ -26,19 +31,26 @@ __device__ unsigned int g_kv_error_word = 0;
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kKeys = 16;  // keys of a warp's group
+constexpr int kKeys = 16;  // keys of a group
+constexpr int kMinGroups = 4;  // fewest groups of a warp's stretch
 constexpr float kRescale = 8.0f;  // log2 units: the maximum may lag by 2^8
 
 struct RowsParams {
     KvArgs a;
     KvPlan p;
     int group;
+    FastDiv dgroup, dpage, dheads, dtokens;  // by group, page_size, H_q, max_tokens
     float scale_log2;
-    float* part_o;    // [split][token][head][D]
-    float* part_lse;  // [split][token][head], log2
-    unsigned items_p;  // blocks over the prefix, the first of the grid
+    float* part_o;    // the tile kernel's partials: [part][token][head][D]
+    float* part_lse;  // [part][token][head], log2
+    float* slot_o;    // the rows kernel's: [slot][row of the tile][D]
+    float* slot_lse;  // [slot][row of the tile], log2
+    int2* meta;       // per j: first slot, number of slots
 };
 
+__device__ __forceinline__ int fdiv(int n, const FastDiv& f) {
+    return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift);
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(valid ? 16 : 0)
@@ -70,6 +82,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Resident blocks of an SM: by registers (16 rows of 64 columns leave room for three).
+constexpr int rows_blocks(int D, int mt) { return D == 64 && mt == 1 ? 3 : 2; }
+
 template <int D, int MT>
 struct RCfg {
     static constexpr int STAGES = D == 128 ? 3 : 4;
@@ -77,8 +92,6 @@ struct RCfg {
     static constexpr int WARP_BYTES = STAGES * 2 * GROUP_BYTES;
     static constexpr int SMEM = kWarps * WARP_BYTES;
     static constexpr int ROWS = MT * 16;
-    static constexpr int PITCH = D + 4;  // floats of a row in the merge buffer
-    static_assert(kWarps * ROWS * PITCH * 4 + kWarps * ROWS * 12 <= SMEM, "merge buffer");
 };
 
 // Byte offset of 16-byte chunk c of row r, chunks permuted within a row so that the eight
@@ -88,111 +101,130 @@ __device__ __forceinline__ uint32_t sw(int r, int c) {
     return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
 }
 
-// A row's place: token index, head, output index (token * H_q + head) or -1.
-struct Row {
-    int tok, head;
+// The line of work.  j: index of a (sequence, head, tile); sequence -1 is the prefix.
+struct Seq {
+    int b, tok0, n_tok, len, groups, tiles;  // groups: 16-key groups of one head and tile
+    const int* table;
 };
 
-// PAGED: keys found through a page table (else dense batch rows).  One page holds whole
-// 16-key groups where PAGE16, else every key is looked up.
+template <int R>
+__device__ __forceinline__ Seq get_seq(const RowsParams& p, int b) {
+    const KvArgs& a = p.a;
+    Seq s;
+    s.b = b;
+    if (b < 0) {
+        s.tok0 = 0;
+        s.n_tok = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;
+        s.len = p.p.kind_p == kKvRows ? a.prefix_len : 0;
+        s.table = a.prefix_table;
+    } else {
+        if (a.cu) {
+            s.tok0 = max(a.cu[b], 0);
+            s.n_tok = min(min(a.cu[b + 1], a.n_tokens) - s.tok0, a.max_tokens);
+        } else {
+            s.tok0 = b * a.max_tokens;
+            s.n_tok = a.max_tokens;
+        }
+        s.len = a.lens ? min(max(a.lens[b], 0), a.max_len) : a.max_len;
+        if (p.p.kind_o != kKvRows) s.len = 0;
+        s.table = a.tables ? a.tables + (long long)b * a.max_pages : nullptr;
+    }
+    s.groups = (s.len + kKeys - 1) / kKeys;
+    s.tiles = s.n_tok > 0 ? (s.n_tok * p.group + R - 1) / R : 0;
+    return s;
+}
+
+// A place on the line: a 16-key group of a (sequence, head, tile).
+struct Place {
+    Seq s;
+    int g, tile, key;  // key: group index
+};
+
+template <int R>
+__device__ __forceinline__ void next_piece(const RowsParams& p, Place& x) {
+    x.key = 0;
+    if (++x.tile < x.s.tiles) return;
+    x.tile = 0;
+    if (++x.g < p.a.H_kv) return;
+    x.g = 0;
+    do {
+        x.s = get_seq<R>(p, x.s.b + 1);
+    } while (x.s.groups * x.s.tiles == 0 && x.s.b + 1 < p.a.B);
+}
+
+// PAGE16: a page holds whole 16-key groups (or the keys are dense); else every key is looked
+// up by itself.
 template <int D, int MT, bool PAGE16>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kernel(const __grid_constant__ RowsParams p) {
     using C = RCfg<D, MT>;
+    constexpr int R = C::ROWS;
     extern __shared__ __align__(128) uint8_t smem[];
     const KvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wid = blockIdx.x * kWarps + warp, n_warps = gridDim.x * kWarps;
 
-    // ---- which rows and keys
-    unsigned item = blockIdx.x;
-    const bool is_prefix = item < p.items_p;
-    int b = 0, split, tile, g, tok0, n_tok, chunk, part;
-    int len;
-    const int* table;
-    if (is_prefix) {
-        tile = item % p.p.tiles_p;
-        item /= p.p.tiles_p;
-        g = item % a.H_kv;
-        split = item / a.H_kv;
-        tok0 = 0;
-        n_tok = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;
-        len = a.prefix_len;
-        chunk = p.p.chunk_p;
-        table = a.prefix_table;
-        part = split;
-    } else {
-        item -= p.items_p;
-        tile = item % p.p.tiles_o;
-        item /= p.p.tiles_o;
-        g = item % a.H_kv;
-        item /= a.H_kv;
-        split = item % p.p.splits_o;
-        b = item / p.p.splits_o;
-        if (a.cu) {
-            tok0 = max(a.cu[b], 0);
-            n_tok = min(a.cu[b + 1], a.n_tokens) - tok0;
-            if (n_tok > a.max_tokens && threadIdx.x == 0 && split == 0)
-                atomicOr(&g_kv_error_word, kKvErrTokens);
-        } else {
-            tok0 = b * a.max_tokens;
-            n_tok = a.max_tokens;
-        }
-        len = a.lens ? max(a.lens[b], 0) : a.max_len;
-        if (len > a.max_len) {
-            if (threadIdx.x == 0 && split == 0) atomicOr(&g_kv_error_word, kKvErrLength);
-            len = a.max_len;
-        }
-        chunk = p.p.chunk_o;
-        table = a.tables ? a.tables + (long long)b * a.max_pages : nullptr;
-        part = p.p.parts_p + split;
-    }
-    const int n_rows = n_tok * p.group;
-    const int row0 = tile * C::ROWS;
-    if (row0 >= n_rows) return;
-    const int k_begin = split * chunk;
-    int k_end = min(k_begin + chunk, len);
-    const bool causal = a.causal && !is_prefix;
-    // the latest key that any of the block's rows sees
-    if (causal) {
-        const int last_tok = min((row0 + C::ROWS - 1) / p.group, n_tok - 1);
-        k_end = min(k_end, len - n_tok + last_tok + 1);
-    }
-    const int n_groups = k_end > k_begin ? (k_end - k_begin + kKeys - 1) / kKeys : 0;
-    const int n_mine = (n_groups - warp + kWarps - 1) / kWarps;  // groups warp, warp + 4, ...
-
-    // ---- Q fragments, straight from global memory
-    const int r_lo = lane >> 2, c_lo = (lane & 3) * 2;
-    uint32_t qf[MT][D / 16][4];
-    int limit[MT][2];  // keys below it are seen
+    // ---- this warp's stretch of the line: [f0, f0 + cnt)
+    Place x;
+    // (the host has checked that the whole line is shorter than 2^31 groups)
+    unsigned per = 0, f0 = 0;
+    int cnt = 0;
+    {
+        auto weight = [&](int b) -> unsigned {
+            if (b >= a.B) return 0;
+            const Seq s = get_seq<R>(p, b);
+            return (unsigned)(s.groups * s.tiles);
+        };
+        const unsigned w_first = weight(lane);  // of the first 32 sequences: read once
+        const unsigned w_prefix = weight(-1);
+        unsigned mine = w_first;
+        for (int b0 = 32; b0 < a.B; b0 += 32) mine += weight(b0 + lane);
+        const unsigned total = (w_prefix + __reduce_add_sync(0xffffffffu, mine)) * a.H_kv;
+        per = max((total + n_warps - 1) / n_warps, (unsigned)kMinGroups);
+        // (a stretch that starts past the end is empty; the product may wrap there)
+        const bool some = wid < (int)((total + per - 1) / per);
+        f0 = per * wid;
+        if (some) {
+            cnt = (int)min(per, total - f0);
+            // the sequence that f0 lies in
+            unsigned at = w_prefix * a.H_kv, rel = f0;
+            int b = -1;
+            if (f0 >= at) {
+                for (int b0 = 0; b0 < a.B; b0 += 32) {
+                    const unsigned w = (b0 == 0 ? w_first : weight(b0 + lane)) * a.H_kv;
+                    unsigned incl = w;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            const int row = row0 + mt * 16 + r_lo + 8 * hf;
-            const bool ok = row < n_rows;
-            const int t = ok ? row / p.group : 0;
-            const int head = g * p.group + (ok ? row - t * p.group : 0);
-            limit[mt][hf] = !ok ? 0 : (causal ? min(k_end, len - n_tok + t + 1) : k_end);
-            const long long off = (a.cu ? (long long)(tok0 + t) * a.q_tstride
-                                        : (long long)b * a.q_bstride + (long long)t * a.q_tstride) +
-                                  (long long)head * D;
-            const uint32_t* q32 = reinterpret_cast<const uint32_t*>((const uint16_t*)a.q + off);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                qf[mt][kk][hf] = ok ? q32[(kk * 16 + c_lo) / 2] : 0u;
-                qf[mt][kk][2 + hf] = ok ? q32[(kk * 16 + c_lo + 8) / 2] : 0u;
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const unsigned y = __shfl_up_sync(0xffffffffu, incl, off);
+                        if (lane >= off) incl += y;
+                    }
+                    const unsigned over = __ballot_sync(0xffffffffu, at + incl > f0);
+                    if (over) {
+                        const int l = __ffs(over) - 1;
+                        b = b0 + l;
+                        rel = f0 - at - __shfl_sync(0xffffffffu, incl - w, l);
+                        break;
+                    }
+                    at += __shfl_sync(0xffffffffu, incl, 31);
+                }
             }
+            x.s = get_seq<R>(p, b);
+            const unsigned piece = rel / (unsigned)x.s.groups;
+            x.key = (int)(rel - piece * (unsigned)x.s.groups);
+            x.g = (int)(piece / (unsigned)x.s.tiles);
+            x.tile = (int)piece - x.g * x.s.tiles;
         }
-    int min_limit = k_end;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        min_limit = min(min_limit, min(limit[mt][0], limit[mt][1]));
-    min_limit = __reduce_min_sync(0xffffffffu, min_limit);
+    }
+    if (cnt == 0) {
+        pdl_wait();
+        return;
+    }
 
-    // ---- loads: group i of this warp is keys k_begin + 16 (warp + 4 i) ..
+    // ---- the loads run ahead of the products on a place of their own
     const uint32_t ring = smem_u32(smem) + warp * C::WARP_BYTES;
-    int page_reg = 0;  // lane l: page of this warp's group 32 (i / 32) + l
-    auto look_up = [&](int key) -> int {
-        int page = table[key / a.page_size];
+    Place y = x;
+    int page_reg = 0, page_at = -1;  // lane l: page of group page_at + l of y's piece
+    auto look_up = [&](const int* table, int key) -> int {
+        int page = table[fdiv(key, p.dpage)];
         if (page < 0 || page >= a.n_pages) {
             atomicOr(&g_kv_error_word, kKvErrPage);
             page = 0;
@@ -200,41 +232,45 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_rows_kernel(const __grid_co
         return page;
     };
     auto load = [&](int i) {
-        if (PAGE16 && table && (i & 31) == 0) {
-            const int ii = i + lane;
-            if (ii < n_mine) page_reg = look_up(k_begin + kKeys * (warp + kWarps * ii));
-        }
-        if (i < n_mine) {
-            const int key0 = k_begin + kKeys * (warp + kWarps * i);
+        if (i < cnt) {
+            const int key0 = y.key * kKeys;
             const uint32_t st = ring + (i % C::STAGES) * 2 * C::GROUP_BYTES;
             long long base = 0;
             if (PAGE16) {
-                if (table) {
-                    const int page = __shfl_sync(0xffffffffu, page_reg, i & 31);
+                if (y.s.table) {
+                    if (page_at < 0 || y.key - page_at >= 32) {
+                        page_at = y.key;
+                        const int kg = page_at + lane;
+                        page_reg = kg < y.s.groups ? look_up(y.s.table, kg * kKeys) : 0;
+                    }
+                    const int page = __shfl_sync(0xffffffffu, page_reg, y.key - page_at);
                     base = (long long)page * a.page_stride +
-                           (long long)(key0 % a.page_size) * a.kv_tstride;
+                           (long long)(key0 - fdiv(key0, p.dpage) * a.page_size) * a.kv_tstride;
                 } else {
-                    base = (long long)b * a.page_stride + (long long)key0 * a.kv_tstride;
+                    base = (long long)y.s.b * a.page_stride + (long long)key0 * a.kv_tstride;
                 }
             }
-            constexpr int CPR = D / 8;          // 16-byte chunks per row
-            constexpr int RPI = 32 / CPR;       // rows per instruction
+            constexpr int CPR = D / 8;     // 16-byte chunks per row
+            constexpr int RPI = 32 / CPR;  // rows per instruction
 #pragma unroll
             for (int r0 = 0; r0 < kKeys; r0 += RPI) {
                 const int r = r0 + lane / CPR, c = lane % CPR;
-                const bool ok = key0 + r < k_end;  // keys past the end: zeros, never read
+                const bool ok = key0 + r < y.s.len;  // keys past the end: zeros, never read
                 long long off;
                 if (PAGE16) {
-                    off = base + (long long)r * a.kv_tstride;
+                    off = base + (ok ? (long long)r * a.kv_tstride : 0);
                 } else {
                     const int key = ok ? key0 + r : key0;
-                    off = (long long)look_up(key) * a.page_stride +
-                          (long long)(key % a.page_size) * a.kv_tstride;
+                    off = (long long)look_up(y.s.table, key) * a.page_stride +
+                          (long long)(key - fdiv(key, p.dpage) * a.page_size) * a.kv_tstride;
                 }
-                off += (long long)g * D + c * 8;
-                if (PAGE16 && !ok) off = base;  // a valid address; nothing is read from it
+                off += (long long)y.g * D + c * 8;
                 cp_async16(st + sw<D>(r, c), (const uint16_t*)a.k + off, ok);
                 cp_async16(st + C::GROUP_BYTES + sw<D>(r, c), (const uint16_t*)a.v + off, ok);
+            }
+            if (++y.key == y.s.groups && i + 1 < cnt) {
+                next_piece<R>(p, y);
+                page_at = -1;
             }
         }
         cp_commit();
@@ -242,45 +278,91 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_rows_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) load(i);
 
+    const int r_lo = lane >> 2, c_lo = (lane & 3) * 2;
+    const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane's address
+    uint32_t qf[MT][D / 16][4];
+    int limit[MT][2];  // keys below it are seen
+    int min_limit = 0;
     float o[MT][D / 8][4];
     float m[MT][2], l[MT][2], lu[MT][2];
+    bool fresh = true;
+    for (int i = 0; i < cnt; ++i) {
+        if (fresh) {  // a new piece: its Q fragments, an empty state
+            fresh = false;
+            const bool causal = a.causal && x.s.b >= 0;
+            min_limit = x.s.len;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int row = x.tile * R + mt * 16 + r_lo + 8 * hf;
+                    const bool ok = row < x.s.n_tok * p.group;
+                    const int t = ok ? fdiv(row, p.dgroup) : 0;
+                    const int head = x.g * p.group + (ok ? row - t * p.group : 0);
+                    limit[mt][hf] = ok && causal ? min(x.s.len, x.s.len - x.s.n_tok + t + 1)
+                                                 : x.s.len;
+                    min_limit = min(min_limit, limit[mt][hf]);
+                    const long long off =
+                        (a.cu ? (long long)(x.s.tok0 + t) * a.q_tstride
+                              : (long long)x.s.b * a.q_bstride + (long long)t * a.q_tstride) +
+                        (long long)head * D;
+                    const uint32_t* q32 =
+                        reinterpret_cast<const uint32_t*>((const uint16_t*)a.q + off);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        qf[mt][kk][hf] = ok ? q32[(kk * 16 + c_lo) / 2] : 0u;
+                        qf[mt][kk][2 + hf] = ok ? q32[(kk * 16 + c_lo + 8) / 2] : 0u;
+                    }
+                    m[mt][hf] = -INFINITY;
+                    l[mt][hf] = lu[mt][hf] = 0.f;
+                }
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            m[mt][hf] = -INFINITY;
-            l[mt][hf] = lu[mt][hf] = 0.f;
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+            }
+            min_limit = __reduce_min_sync(0xffffffffu, min_limit);
+            if (x.key == 0 && lane == 0) {  // the piece that starts this j: note its slots
+                const unsigned last = (f0 + i + x.s.groups - 1) / per;
+                const int j = x.s.b < 0 ? x.g * p.p.tiles_p + x.tile
+                                        : p.p.j_own + (x.s.b * a.H_kv + x.g) * p.p.tiles_o + x.tile;
+                p.meta[j] = make_int2(wid + j, (int)last - wid + 1);
+            }
         }
-    }
-    const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane's address
-    for (int i = 0; i < n_mine; ++i) {
         cp_wait<C::STAGES - 2>();
         __syncwarp();
         load(i + C::STAGES - 1);
         const uint32_t kst = ring + (i % C::STAGES) * 2 * C::GROUP_BYTES;
         const uint32_t vst = kst + C::GROUP_BYTES;
-        float s[MT][2][4];
+        // two accumulation chains (even and odd steps of D) where registers allow: with two
+        // warps to a scheduler the products' latency shows
+        constexpr int CHAINS = D == 128 && MT == 2 ? 1 : 2;
+        float s[MT][2][4], s_odd[MT][2][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[mt][n][e] = s_odd[mt][n][e] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t kf[4];
             ldsm4(kf, kst + sw<D>((mi >> 1) * 8 + mr, kk * 2 + (mi & 1)));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                mma16816(s[mt][0], qf[mt][kk], kf[0], kf[1]);
-                mma16816(s[mt][1], qf[mt][kk], kf[2], kf[3]);
+                float(&acc)[2][4] = CHAINS == 2 && (kk & 1) ? s_odd[mt] : s[mt];
+                mma16816(acc[0], qf[mt][kk], kf[0], kf[1]);
+                mma16816(acc[1], qf[mt][kk], kf[2], kf[3]);
             }
         }
-        const int key0 = k_begin + kKeys * (warp + kWarps * i);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (CHAINS == 2) s[mt][n][e] += s_odd[mt][n][e];
+        const int key0 = x.key * kKeys;
         if (key0 + kKeys > min_limit) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -345,168 +427,228 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_rows_kernel(const __grid_co
                 mma16816(o[mt][2 * nn + 1], pf[mt], vf[2], vf[3]);
             }
         }
+        // ---- the piece's end: its partial result
+        const bool border = x.key + 1 == x.s.groups;
+        if (border || i + 1 == cnt) {
+            const int j = x.s.b < 0 ? x.g * p.p.tiles_p + x.tile
+                                    : p.p.j_own + (x.s.b * a.H_kv + x.g) * p.p.tiles_o + x.tile;
+            const long long slot = (long long)(wid + j) * R;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                    for (int off = 1; off <= 2; off <<= 1) {
+                        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], off);
+                        lu[mt][hf] += __shfl_xor_sync(0xffffffffu, lu[mt][hf], off);
+                    }
+                    const int r = mt * 16 + r_lo + 8 * hf;
+                    if (x.tile * R + r < x.s.n_tok * p.group) {
+                        // no key seen: every m is -inf and every sum 0 (a NaN score leaves m
+                        // as it was but makes the sums NaN, which must come through)
+                        const float inv = lu[mt][hf] == 0.f ? 0.f : 1.f / lu[mt][hf];
+                        float* dst = p.slot_o + (slot + r) * D + c_lo;
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n)
+                            *reinterpret_cast<float2*>(dst + n * 8) =
+                                make_float2(o[mt][n][2 * hf] * inv, o[mt][n][2 * hf + 1] * inv);
+                        if ((lane & 3) == 0)
+                            p.slot_lse[slot + r] =
+                                l[mt][hf] == 0.f
+                                    ? -INFINITY
+                                    : (m[mt][hf] == -INFINITY ? 0.f : m[mt][hf]) + log2f(l[mt][hf]);
+                    }
+                }
+            fresh = true;
+        }
+        ++x.key;
+        if (border && i + 1 < cnt) next_piece<R>(p, x);
         __syncwarp();
     }
-    cp_wait<0>();
-    __syncthreads();
-
-    // ---- merge the warps' states through shared memory
-    float* so = reinterpret_cast<float*>(smem);               // [warp][row][PITCH]
-    float* sm = so + kWarps * C::ROWS * C::PITCH;             // [warp][row][3]: m, l, lu
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-            for (int off = 1; off <= 2; off <<= 1) {
-                l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], off);
-                lu[mt][hf] += __shfl_xor_sync(0xffffffffu, lu[mt][hf], off);
-            }
-            const int r = mt * 16 + r_lo + 8 * hf;
-            float* w = so + (warp * C::ROWS + r) * C::PITCH;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-                *reinterpret_cast<float2*>(w + n * 8 + c_lo) =
-                    make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
-            if ((lane & 3) == 0) {
-                float* x = sm + (warp * C::ROWS + r) * 3;
-                x[0] = m[mt][hf];
-                x[1] = l[mt][hf];
-                x[2] = lu[mt][hf];
-            }
-        }
-    __syncthreads();
-    constexpr int TPR = D / 4;  // threads per row
-    for (int r = threadIdx.x / TPR; r < C::ROWS; r += kWarps * 32 / TPR) {
-        const int row = row0 + r, c = (threadIdx.x % TPR) * 4;
-        if (row >= n_rows) break;
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm[(w * C::ROWS + r) * 3]);
-        float ls = 0.f, lus = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        // a row that saw nothing has every m = -inf and every sum 0; a NaN score leaves m
-        // at -inf as well but makes the sums NaN, which must come through
-        const float ms = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float* x = sm + (w * C::ROWS + r) * 3;
-            const float f = ex2_approx(x[0] - ms);
-            ls += f * x[1];
-            lus += f * x[2];
-            const float4 v =
-                *reinterpret_cast<const float4*>(so + (w * C::ROWS + r) * C::PITCH + c);
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
-        }
-        const float inv = lus == 0.f ? 0.f : 1.f / lus;
-        const float lse2 = ls == 0.f ? -INFINITY : ms + log2f(ls);
-        acc.x *= inv;
-        acc.y *= inv;
-        acc.z *= inv;
-        acc.w *= inv;
-        const int t = row / p.group, head = g * p.group + row - t * p.group;
-        const long long orow = (long long)(tok0 + t) * a.H_q + head;
-        if (p.p.direct) {
-            if (a.out_bf16)
-                *reinterpret_cast<uint2*>((uint16_t*)a.out + orow * D + c) =
-                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            else
-                *reinterpret_cast<float4*>((float*)a.out + orow * D + c) = acc;
-            if (c == 0) {
-                const long long li = a.cu ? (long long)head * a.n_tokens + tok0 + t
-                                          : ((long long)b * a.H_q + head) * a.max_tokens + t;
-                a.lse[li] = lse2 * 0.69314718055994530942f;
-            }
-        } else {
-            const long long pr = (long long)part * a.n_tokens * a.H_q + orow;
-            if (lse2 != -INFINITY)
-                *reinterpret_cast<float4*>(p.part_o + pr * D + c) = acc;
-            if (c == 0) p.part_lse[pr] = lse2;
-        }
-    }
+    pdl_launch_dependents();
+    pdl_wait();  // so that this grid's end means the tile kernel's end too
 }
 
-// One warp per row: its partials' log2 sums give the weights, and the weighted outputs are
-// added up in ascending order of the splits (the same bits on every call).
+// One warp per row: its partials' log2 sums give the weights, one lane each, and the
+// weighted outputs are added up in the splits' order (the same bits on every call), 16 bytes
+// a lane: whole rows of D = 128, two partials at a time of D = 64.  It lives on latency (a
+// row's partials are some KB in L2), so eight partials' loads are in flight at once.
 template <int D>
-__global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__ RowsParams p) {
     const KvArgs& a = p.a;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int idx = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5);  // below 2^31 + 8: checked
     const int lane = threadIdx.x & 31;
     const long long rows = (long long)a.n_tokens * a.H_q;
-    if (row >= rows) return;
-    const int tok = (int)(row / a.H_q), head = (int)(row - (long long)tok * a.H_q);
-    if (a.cu && tok >= a.cu[a.B]) return;  // rows behind the last sequence stay as they were
-    const int ns = p.p.parts_p + p.p.parts_o;
-    float mm = -INFINITY;
-    for (int s = lane; s < ns; s += 32) mm = fmaxf(mm, p.part_lse[s * rows + row]);
+    const int R = 16 * p.p.mt;
+    // the row: by token, or by (sequence, its token) where the rows kernel took the own keys
+    const int i_tok = fdiv(idx, p.dheads), head = idx - i_tok * a.H_q;
+    int b = 0, t = 0, tok = i_tok;
+    bool live;
+    const int end = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;  // rows from here on stay
+    if (p.p.kind_o == kKvRows) {
+        b = fdiv(i_tok, p.dtokens);
+        t = i_tok - b * a.max_tokens;
+        live = b < a.B;
+        if (live && a.cu) {
+            const int c0 = max(a.cu[b], 0), n = min(a.cu[b + 1], a.n_tokens) - c0;
+            if (n > a.max_tokens && t == 0 && head == 0 && lane == 0)
+                atomicOr(&g_kv_error_word, kKvErrTokens);
+            tok = c0 + t;
+            live = t < n && tok < end;
+        }
+    } else {
+        live = tok < end;
+    }
+    if (!live) {
+        pdl_wait();  // the end of this grid has to mean the end of those before it
+        return;
+    }
+    const long long row = (long long)tok * a.H_q + head;
+    const int g = fdiv(head, p.dgroup), hh = head - g * p.group;
+    // two runs of partials: the prefix's, then the own keys'
+    int n1 = 0, n2 = 0;
+    const float *o1 = nullptr, *o2 = nullptr, *l1 = nullptr, *l2 = nullptr;
+    long long s1 = rows, s2 = rows;  // rows between a run's partials
+    int len = 0;
+    if (p.p.kind_o == kKvRows) {
+        len = a.lens ? a.lens[b] : a.max_len;
+        if (len > a.max_len && t == 0 && head == 0 && lane == 0)
+            atomicOr(&g_kv_error_word, kKvErrLength);
+    }
+    pdl_wait();
+    auto slots_of = [&](int j) {  // in bounds even if the batch changed under the call
+        int2 x = p.meta[j];
+        x.x = min(max(x.x, 0), (int)p.p.slots - 1);
+        x.y = min(max(x.y, 0), (int)p.p.slots - x.x);
+        return x;
+    };
+    if (p.p.kind_p == kKvTiles) {
+        n1 = p.p.parts_p;
+        o1 = p.part_o + row * D;
+        l1 = p.part_lse + row;
+    } else if (p.p.kind_p == kKvRows) {
+        const int r = tok * p.group + hh;
+        const int2 mt = slots_of(g * p.p.tiles_p + r / R);
+        n1 = mt.y;
+        s1 = R;
+        o1 = p.slot_o + ((long long)mt.x * R + r % R) * D;
+        l1 = p.slot_lse + (long long)mt.x * R + r % R;
+    }
+    if (p.p.kind_o == kKvTiles) {
+        n2 = p.p.parts_o;
+        o2 = p.part_o + (p.p.parts_p * rows + row) * D;
+        l2 = p.part_lse + p.p.parts_p * rows + row;
+    } else if (len > 0) {
+        const int r = t * p.group + hh;
+        const int2 mt = slots_of(p.p.j_own + (b * a.H_kv + g) * p.p.tiles_o + r / R);
+        n2 = mt.y;
+        s2 = R;
+        o2 = p.slot_o + ((long long)mt.x * R + r % R) * D;
+        l2 = p.slot_lse + (long long)mt.x * R + r % R;
+    }
+    const int ns = n1 + n2;
+    auto lse_of = [&](int s) { return s < n1 ? l1[s * s1] : l2[(s - n1) * s2]; };
+    const float first = lane < ns ? lse_of(lane) : -INFINITY;
+    float mm = first;
+    for (int s = lane + 32; s < ns; s += 32) mm = fmaxf(mm, lse_of(s));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
-    constexpr int V = D / 32;  // values per lane
-    float acc[V], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
     const float ms = mm == -INFINITY ? 0.f : mm;  // (a NaN partial comes through as NaN)
-    for (int s = 0; s < ns; ++s) {
-        const float w = ex2_approx(p.part_lse[s * rows + row] - ms);
-        if (w == 0.f) continue;  // an empty partial has no output either
+    constexpr int LPR = D / 4;    // lanes of a row
+    constexpr int PAR = 32 / LPR;  // partials at a time
+    const int sub = lane / LPR, c = (lane % LPR) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int base = 0; base < ns; base += 32) {
+        const float x = base == 0 ? first
+                        : base + lane < ns ? lse_of(base + lane) : -INFINITY;
+        const float w = ex2_approx(x - ms);
         sum += w;
-        const float* src = p.part_o + (s * rows + row) * D + lane * V;
+        const int m = min(32, ns - base);
+        for (int j = 0; j < m; j += 8 * PAR) {
+            float wj[8];
+            float4 v[8];
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+            for (int u = 0; u < 8; ++u) {
+                const int k = j + u * PAR + sub;
+                wj[u] = __shfl_sync(0xffffffffu, w, k & 31);
+                if (k >= m) wj[u] = 0.f;
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wj[u] != 0.f) {  // an empty partial adds nothing
+                    const int q = base + k;
+                    v[u] = *reinterpret_cast<const float4*>(
+                        (q < n1 ? o1 + q * s1 * D : o2 + (q - n1) * s2 * D) + c);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                acc.x = fmaf(wj[u], v[u].x, acc.x);
+                acc.y = fmaf(wj[u], v[u].y, acc.y);
+                acc.z = fmaf(wj[u], v[u].z, acc.z);
+                acc.w = fmaf(wj[u], v[u].w, acc.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (PAR == 2) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] *= inv;
-    if (a.out_bf16) {
-        uint32_t* dst = reinterpret_cast<uint32_t*>((uint16_t*)a.out + row * D + lane * V);
-#pragma unroll
-        for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16x2(acc[e], acc[e + 1]);
-    } else {
-        float* dst = (float*)a.out + row * D + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) dst[e] = acc[e];
+    if (sub == 0) {
+        if (a.out_bf16)
+            *reinterpret_cast<uint2*>((uint16_t*)a.out + row * D + c) =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                           pack_bf16x2(acc.z * inv, acc.w * inv));
+        else
+            *reinterpret_cast<float4*>((float*)a.out + row * D + c) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
     if (lane == 0) {
         long long li;
         if (a.cu) {
             li = (long long)head * a.n_tokens + tok;
         } else {
-            const int b = tok / a.max_tokens, t = tok - b * a.max_tokens;
-            li = ((long long)b * a.H_q + head) * a.max_tokens + t;
+            const int bb = fdiv(tok, p.dtokens), tt = tok - bb * a.max_tokens;
+            li = ((long long)bb * a.H_q + head) * a.max_tokens + tt;
         }
         a.lse[li] = sum == 0.f ? -INFINITY : (ms + log2f(sum)) * 0.69314718055994530942f;
     }
 }
 
+// Launches the second or a later kernel of a call: with `overlap` its blocks may start once
+// the kernel before it has no block left to start (programmatic dependent launch).  The rows
+// kernel reads nothing that the tile kernel writes, and waits for it only before it ends;
+// the combine waits before it reads.
+template <typename K>
+cudaError_t launch_pdl(K kernel, const RowsParams& p, unsigned grid, int threads, int smem,
+                       cudaStream_t stream, bool overlap) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <int D, int MT, bool PAGE16>
-cudaError_t launch_rows(const RowsParams& p, unsigned grid) {
+cudaError_t launch_rows(const RowsParams& p, unsigned grid, bool after_tiles) {
     using C = RCfg<D, MT>;
     auto k = kv_rows_kernel<D, MT, PAGE16>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    k<<<grid, kWarps * 32, C::SMEM, p.a.stream>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(k, p, grid, kWarps * 32, C::SMEM, p.a.stream, after_tiles);
 }
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
-
-// Keys per split: about `target` blocks in all, no split under 128 keys (four warps of two
-// groups), a multiple of 64.
-int chunk_for(long long blocks_per_split, int keys, long long target) {
-    long long splits = target / (blocks_per_split > 0 ? blocks_per_split : 1);
-    if (splits < 1) splits = 1;
-    long long chunk = (keys + splits - 1) / splits;
-    chunk = (chunk + 63) / 64 * 64;
-    return (int)(chunk < 128 ? 128 : chunk);
-}
-
-}  // namespace
-
-namespace {
 
 // The tile kernel's share of a plan over `units` (batch rows) x H_kv heads, `tokens` tokens
 // and `keys` keys each: row blocks, and the number of key ranges that takes the least time
@@ -556,34 +698,48 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
                                                                        : rows_p;
     p.mt = rows_most > 16 ? 2 : 1;
     const int R = 16 * p.mt;
+    long long groups = 0;  // the rows kernel's work, at most
     if (p.kind_p == kKvRows) {
         p.tiles_p = ceil_div(rows_p, R);
-        p.chunk_p = chunk_for((long long)H_kv * p.tiles_p, prefix_len, 4LL * kSms);
-        p.splits_p = p.parts_p = ceil_div(prefix_len, p.chunk_p);
+        groups += (long long)ceil_div(prefix_len, kKeys) * p.tiles_p * H_kv;
     } else if (p.kind_p == kKvTiles) {
         plan_tiles(1, H_kv, group, n_tokens, prefix_len, D, part_bytes, true, p.chunk_p,
                    p.splits_p, p.tiles_p, p.ksplit_p, p.parts_p);
     }
     if (p.kind_o == kKvRows) {
         p.tiles_o = ceil_div(rows_o, R);
-        p.chunk_o = chunk_for((long long)B * H_kv * p.tiles_o, max_len, 8LL * kSms);
-        p.splits_o = p.parts_o = ceil_div(max_len, p.chunk_o);
+        groups += (long long)B * ceil_div(max_len, kKeys) * p.tiles_o * H_kv;
     } else {
         plan_tiles(B, H_kv, group, max_tokens, max_len, D, part_bytes, p.kind_p != kKvNone,
                    p.chunk_o, p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
     }
-    p.direct = p.parts_p + p.parts_o == 1;
-    const long long bp = (long long)p.splits_p * H_kv * p.tiles_p,
-                    bo = (long long)B * p.splits_o * H_kv * p.tiles_o;
-    p.blocks = bp + bo;
-    p.workspace = p.direct ? 0 : (p.parts_p + p.parts_o) * part_bytes;
+    p.direct = p.kind_p == kKvNone && p.kind_o == kKvTiles && p.parts_o == 1;
+    p.blocks = (p.kind_p == kKvTiles ? (long long)p.splits_p * H_kv * p.tiles_p : 0) +
+               (p.kind_o == kKvTiles ? (long long)B * p.splits_o * H_kv * p.tiles_o : 0);
+    long long bytes = p.direct ? 0 : (p.parts_p + p.parts_o) * part_bytes;
+    if (groups > 0) {
+        const long long blocks = (groups + kMinGroups * kWarps - 1) / (kMinGroups * kWarps);
+        const int most = rows_blocks(D, p.mt) * kSms;
+        p.row_blocks = (int)(blocks < most ? blocks : most);
+        p.j_own = p.kind_p == kKvRows ? H_kv * p.tiles_p : 0;
+        const long long js =
+            p.j_own + (p.kind_o == kKvRows ? (long long)B * H_kv * p.tiles_o : 0);
+        p.slots = (long long)p.row_blocks * kWarps + js;
+        bytes += p.slots * R * (D + 1) * 4 + js * 8 + 32;
+        const long long rows = (long long)B * max_tokens * H_q;  // the combine's, at most
+        if (p.blocks < p.slots) p.blocks = p.slots;
+        if (p.blocks < rows) p.blocks = rows;
+        if (p.blocks < groups) p.blocks = groups;
+    }
+    p.workspace = bytes;
     return p;
 }
 
 cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wait_limit_ns,
                       const char** why) {
     cudaError_t e = cudaSuccess;
-    if (plan.kind_p == kKvTiles || plan.kind_o == kKvTiles) {
+    const bool tiled = plan.kind_p == kKvTiles || plan.kind_o == kKvTiles;
+    if (tiled) {
         e = launch_kv_tiles(a, plan, wait_limit_ns, why);
         if (e != cudaSuccess) return e;
     }
@@ -591,36 +747,39 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
     p.a = a;
     p.p = plan;
     p.group = a.H_q / a.H_kv;
+    p.dgroup = make_fastdiv((uint32_t)p.group);
+    p.dpage = make_fastdiv((uint32_t)a.page_size);
+    p.dheads = make_fastdiv((uint32_t)a.H_q);
+    p.dtokens = make_fastdiv((uint32_t)a.max_tokens);
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     const long long rows = (long long)a.n_tokens * a.H_q;
     p.part_o = (float*)a.workspace;
     p.part_lse = p.part_o + (long long)(plan.parts_p + plan.parts_o) * rows * a.D;
-    p.items_p = plan.kind_p == kKvRows
-                    ? (unsigned)((long long)plan.splits_p * a.H_kv * plan.tiles_p)
-                    : 0;
-    const unsigned grid =
-        p.items_p + (plan.kind_o == kKvRows
-                         ? (unsigned)((long long)a.B * plan.splits_o * a.H_kv * plan.tiles_o)
-                         : 0);
-    if (grid > 0) {
+    if (plan.row_blocks > 0) {
+        float* after = p.part_lse + (long long)(plan.parts_p + plan.parts_o) * rows;
+        p.slot_o = (float*)(((uintptr_t)after + 15) & ~(uintptr_t)15);
+        p.slot_lse = p.slot_o + plan.slots * 16 * plan.mt * a.D;
+        p.meta = (int2*)(p.slot_lse + plan.slots * 16 * plan.mt);
+        const unsigned grid = (unsigned)plan.row_blocks;
         const bool page16 = !a.tables || a.page_size % kKeys == 0;
         if (a.D == 128) {
             if (plan.mt == 1)
-                e = page16 ? launch_rows<128, 1, true>(p, grid) : launch_rows<128, 1, false>(p, grid);
+                e = page16 ? launch_rows<128, 1, true>(p, grid, tiled) : launch_rows<128, 1, false>(p, grid, tiled);
             else
-                e = page16 ? launch_rows<128, 2, true>(p, grid) : launch_rows<128, 2, false>(p, grid);
+                e = page16 ? launch_rows<128, 2, true>(p, grid, tiled) : launch_rows<128, 2, false>(p, grid, tiled);
         } else {
             if (plan.mt == 1)
-                e = page16 ? launch_rows<64, 1, true>(p, grid) : launch_rows<64, 1, false>(p, grid);
+                e = page16 ? launch_rows<64, 1, true>(p, grid, tiled) : launch_rows<64, 1, false>(p, grid, tiled);
             else
-                e = page16 ? launch_rows<64, 2, true>(p, grid) : launch_rows<64, 2, false>(p, grid);
+                e = page16 ? launch_rows<64, 2, true>(p, grid, tiled) : launch_rows<64, 2, false>(p, grid, tiled);
         }
     }
     if (e != cudaSuccess || plan.direct) return e;
-    const unsigned cg = (unsigned)((rows + 3) / 4);
-    if (a.D == 128) kv_combine_kernel<128><<<cg, 128, 0, a.stream>>>(p);
-    else kv_combine_kernel<64><<<cg, 128, 0, a.stream>>>(p);
-    return cudaGetLastError();
+    const long long out_rows =
+        plan.kind_o == kKvRows ? (long long)a.B * a.max_tokens * a.H_q : rows;
+    const unsigned cg = (unsigned)((out_rows + 7) / 8);
+    return a.D == 128 ? launch_pdl(kv_combine_kernel<128>, p, cg, 256, 0, a.stream, true)
+                      : launch_pdl(kv_combine_kernel<64>, p, cg, 256, 0, a.stream, true);
 }
 
 cudaError_t read_and_clear_kv_error(unsigned int* value) {

@@ -576,6 +576,12 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_tiles_sm100(const __grid_constant__ TileParams p) {
     using C = Cfg<D>;
     Item x;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&p.tm_q);
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
+    pdl_launch_dependents();  // the rows kernel, which waits for this one only at its end
     if (!make_item(p, x)) return;  // the same for every thread of the block
     extern __shared__ uint8_t smem_raw[];
     uint32_t base = smem_u32(smem_raw);

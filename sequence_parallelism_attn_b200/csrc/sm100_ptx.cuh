@@ -316,6 +316,18 @@ __device__ __forceinline__ void regs_decrease() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ------------------------------------------------------------------ dependent launches
+// Programmatic dependent launch: the next kernel of the stream, launched for it, may start
+// its blocks once every block of this one has called pdl_launch_dependents (or ended);
+// pdl_wait returns once the kernel before this one has ended and its writes are visible (at
+// once for a kernel that was launched plainly).
+__device__ __forceinline__ void pdl_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ math
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
