@@ -122,21 +122,6 @@ def usp_attention_dist(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal
                                    float(scale), ulysses_group, ring_group)
 
 
-class _CrossAttention(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, v, kv_lens, scale):
-        o, lse = ra.cross_attn_fwd(q, k, v, kv_lens, scale, out_dtype=q.dtype)
-        ctx.save_for_backward(q, k, v, o, lse, kv_lens)
-        ctx.scale = scale
-        return o
-
-    @staticmethod
-    def backward(ctx, do):
-        q, k, v, o, lse, kv_lens = ctx.saved_tensors
-        return (*ra.cross_attn_bwd(q, k, v, o, lse, do.contiguous(), kv_lens, ctx.scale,
-                                   grad_dtype=q.dtype), None, None)
-
-
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     kv_lens: torch.Tensor | None = None,
                     scale: float | None = None) -> torch.Tensor:
@@ -148,4 +133,6 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         raise ValueError("the differentiable path takes bf16 inputs (the tensor-core backward)")
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    return _CrossAttention.apply(q, k, v, kv_lens, float(scale))
+    # (a C++ node: a Python backward costs 90 us on autograd's thread, several times a short
+    # sample's kernels)
+    return ra.native().cross_attention(q, k, v, kv_lens, float(scale))

@@ -1,7 +1,7 @@
 // kv_rows.cu -- attention of few query rows over many keys: the single-token form of the
 // paged, prefix and cross attention, and the joining of every form's partial results.
 //
-// Work is counted in 16-key groups of (sequence, kv head, row tile) -- row tiles of 16 or 32
+// Work is counted in groups of 16 keys (32 at D = 64) of (sequence, kv head, row tile) -- row tiles of 16 or 32
 // rows, tokens x the query heads that share the kv head -- laid end to end: the prefix first
 // (rows of the whole batch, so its keys are read once), then every sequence's own keys.  The
 // resident warps (four to a block, two blocks to an SM) each take an equal stretch of that
@@ -31,7 +31,9 @@ __device__ unsigned int g_kv_error_word = 0;
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kKeys = 16;  // keys of a group
+// Keys of a group: 8 KB of K and V either way.  At D = 64 a group of 16 spent as much on the
+// softmax's latencies as on its bytes (5.5 TB/s in the long run, against 6.2 at D = 128).
+constexpr int group_keys(int D) { return D == 64 ? 32 : 16; }
 constexpr int kMinGroups = 4;  // fewest groups of a warp's stretch
 constexpr float kRescale = 8.0f;  // log2 units: the maximum may lag by 2^8
 
@@ -82,13 +84,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Resident blocks of an SM: by registers (16 rows of 64 columns leave room for three).
-constexpr int rows_blocks(int D, int mt) { return D == 64 && mt == 1 ? 3 : 2; }
+constexpr int kBlocksPerSm = 2;  // resident, by registers and by the rings' 96 KB
 
 template <int D, int MT>
 struct RCfg {
-    static constexpr int STAGES = D == 128 ? 3 : 4;
-    static constexpr int GROUP_BYTES = kKeys * D * 2;          // K or V of one group
+    static constexpr int STAGES = 3;
+    static constexpr int KEYS = group_keys(D);
+    static constexpr int GROUP_BYTES = KEYS * D * 2;           // K or V of one group
     static constexpr int WARP_BYTES = STAGES * 2 * GROUP_BYTES;
     static constexpr int SMEM = kWarps * WARP_BYTES;
     static constexpr int ROWS = MT * 16;
@@ -103,11 +105,11 @@ __device__ __forceinline__ uint32_t sw(int r, int c) {
 
 // The line of work.  j: index of a (sequence, head, tile); sequence -1 is the prefix.
 struct Seq {
-    int b, tok0, n_tok, len, groups, tiles;  // groups: 16-key groups of one head and tile
+    int b, tok0, n_tok, len, groups, tiles;  // groups: key groups of one head and tile
     const int* table;
 };
 
-template <int R>
+template <int R, int KEYS>
 __device__ __forceinline__ Seq get_seq(const RowsParams& p, int b) {
     const KvArgs& a = p.a;
     Seq s;
@@ -129,18 +131,18 @@ __device__ __forceinline__ Seq get_seq(const RowsParams& p, int b) {
         if (p.p.kind_o != kKvRows) s.len = 0;
         s.table = a.tables ? a.tables + (long long)b * a.max_pages : nullptr;
     }
-    s.groups = (s.len + kKeys - 1) / kKeys;
+    s.groups = (s.len + KEYS - 1) / KEYS;
     s.tiles = s.n_tok > 0 ? (s.n_tok * p.group + R - 1) / R : 0;
     return s;
 }
 
-// A place on the line: a 16-key group of a (sequence, head, tile).
+// A place on the line: a key group of a (sequence, head, tile).
 struct Place {
     Seq s;
     int g, tile, key;  // key: group index
 };
 
-template <int R>
+template <int R, int KEYS>
 __device__ __forceinline__ void next_piece(const RowsParams& p, Place& x) {
     x.key = 0;
     if (++x.tile < x.s.tiles) return;
@@ -148,16 +150,16 @@ __device__ __forceinline__ void next_piece(const RowsParams& p, Place& x) {
     if (++x.g < p.a.H_kv) return;
     x.g = 0;
     do {
-        x.s = get_seq<R>(p, x.s.b + 1);
+        x.s = get_seq<R, KEYS>(p, x.s.b + 1);
     } while (x.s.groups * x.s.tiles == 0 && x.s.b + 1 < p.a.B);
 }
 
-// PAGE16: a page holds whole 16-key groups (or the keys are dense); else every key is looked
+// PAGE16: a page holds whole runs of 16 keys (or the keys are dense); else every key is looked
 // up by itself.
 template <int D, int MT, bool PAGE16>
-__global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(const __grid_constant__ RowsParams p) {
     using C = RCfg<D, MT>;
-    constexpr int R = C::ROWS;
+    constexpr int R = C::ROWS, kKeys = C::KEYS, NT = kKeys / 8, H16 = kKeys / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     const KvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
     {
         auto weight = [&](int b) -> unsigned {
             if (b >= a.B) return 0;
-            const Seq s = get_seq<R>(p, b);
+            const Seq s = get_seq<R, C::KEYS>(p, b);
             return (unsigned)(s.groups * s.tiles);
         };
         const unsigned w_first = weight(lane);  // of the first 32 sequences: read once
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
                     at += __shfl_sync(0xffffffffu, incl, 31);
                 }
             }
-            x.s = get_seq<R>(p, b);
+            x.s = get_seq<R, C::KEYS>(p, b);
             const unsigned piece = rel / (unsigned)x.s.groups;
             x.key = (int)(rel - piece * (unsigned)x.s.groups);
             x.g = (int)(piece / (unsigned)x.s.tiles);
@@ -215,14 +217,14 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
         }
     }
     if (cnt == 0) {
-        pdl_wait();
+        if (blockIdx.x == 0) pdl_wait();
         return;
     }
 
     // ---- the loads run ahead of the products on a place of their own
     const uint32_t ring = smem_u32(smem) + warp * C::WARP_BYTES;
     Place y = x;
-    int page_reg = 0, page_at = -1;  // lane l: page of group page_at + l of y's piece
+    int page_reg = 0, page_at = -1;  // lane l: page of the piece's 16 keys number page_at + l
     auto look_up = [&](const int* table, int key) -> int {
         int page = table[fdiv(key, p.dpage)];
         if (page < 0 || page >= a.n_pages) {
@@ -235,41 +237,48 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
         if (i < cnt) {
             const int key0 = y.key * kKeys;
             const uint32_t st = ring + (i % C::STAGES) * 2 * C::GROUP_BYTES;
-            long long base = 0;
-            if (PAGE16) {
-                if (y.s.table) {
-                    if (page_at < 0 || y.key - page_at >= 32) {
-                        page_at = y.key;
-                        const int kg = page_at + lane;
-                        page_reg = kg < y.s.groups ? look_up(y.s.table, kg * kKeys) : 0;
-                    }
-                    const int page = __shfl_sync(0xffffffffu, page_reg, y.key - page_at);
-                    base = (long long)page * a.page_stride +
-                           (long long)(key0 - fdiv(key0, p.dpage) * a.page_size) * a.kv_tstride;
-                } else {
-                    base = (long long)y.s.b * a.page_stride + (long long)key0 * a.kv_tstride;
-                }
+            if (PAGE16 && y.s.table && (page_at < 0 || y.key * H16 - page_at >= 32)) {
+                page_at = y.key * H16;
+                const int key = (page_at + lane) * 16;
+                page_reg = key < y.s.len ? look_up(y.s.table, key) : 0;
             }
             constexpr int CPR = D / 8;     // 16-byte chunks per row
             constexpr int RPI = 32 / CPR;  // rows per instruction
 #pragma unroll
-            for (int r0 = 0; r0 < kKeys; r0 += RPI) {
-                const int r = r0 + lane / CPR, c = lane % CPR;
-                const bool ok = key0 + r < y.s.len;  // keys past the end: zeros, never read
-                long long off;
+            for (int h = 0; h < H16; ++h) {
+                const int first = key0 + 16 * h;
+                long long base = 0;
                 if (PAGE16) {
-                    off = base + (ok ? (long long)r * a.kv_tstride : 0);
-                } else {
-                    const int key = ok ? key0 + r : key0;
-                    off = (long long)look_up(y.s.table, key) * a.page_stride +
-                          (long long)(key - fdiv(key, p.dpage) * a.page_size) * a.kv_tstride;
+                    if (y.s.table) {
+                        const int page =
+                            __shfl_sync(0xffffffffu, page_reg, y.key * H16 + h - page_at);
+                        base = (long long)page * a.page_stride +
+                               (long long)(first - fdiv(first, p.dpage) * a.page_size) * a.kv_tstride;
+                    } else {
+                        base = (long long)y.s.b * a.page_stride + (long long)first * a.kv_tstride;
+                    }
+                    if (first >= y.s.len) base = 0;  // no key there: nothing is read
                 }
-                off += (long long)y.g * D + c * 8;
-                cp_async16(st + sw<D>(r, c), (const uint16_t*)a.k + off, ok);
-                cp_async16(st + C::GROUP_BYTES + sw<D>(r, c), (const uint16_t*)a.v + off, ok);
+#pragma unroll
+                for (int r0 = 0; r0 < 16; r0 += RPI) {
+                    const int r = r0 + lane / CPR, c = lane % CPR;
+                    const bool ok = first + r < y.s.len;  // keys past the end: zeros, not read
+                    long long off;
+                    if (PAGE16) {
+                        off = base + (ok ? (long long)r * a.kv_tstride : 0);
+                    } else {
+                        const int key = ok ? first + r : key0;
+                        off = (long long)look_up(y.s.table, key) * a.page_stride +
+                              (long long)(key - fdiv(key, p.dpage) * a.page_size) * a.kv_tstride;
+                    }
+                    off += (long long)y.g * D + c * 8;
+                    const uint32_t dst = st + sw<D>(16 * h + r, c);
+                    cp_async16(dst, (const uint16_t*)a.k + off, ok);
+                    cp_async16(dst + C::GROUP_BYTES, (const uint16_t*)a.v + off, ok);
+                }
             }
             if (++y.key == y.s.groups && i + 1 < cnt) {
-                next_piece<R>(p, y);
+                next_piece<R, C::KEYS>(p, y);
                 page_at = -1;
             }
         }
@@ -334,54 +343,57 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
         load(i + C::STAGES - 1);
         const uint32_t kst = ring + (i % C::STAGES) * 2 * C::GROUP_BYTES;
         const uint32_t vst = kst + C::GROUP_BYTES;
-        // two accumulation chains (even and odd steps of D) where registers allow: with two
-        // warps to a scheduler the products' latency shows
-        constexpr int CHAINS = D == 128 && MT == 2 ? 1 : 2;
-        float s[MT][2][4], s_odd[MT][2][4];
+        // two accumulation chains (even and odd steps of D) of a 16-key group where registers
+        // allow: with two warps to a scheduler the products' latency shows
+        constexpr int CHAINS = D == 128 && MT == 1 ? 2 : 1;
+        float s[MT][NT][4], s_odd[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[mt][n][e] = s_odd[mt][n][e] = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t kf[4];
-            ldsm4(kf, kst + sw<D>((mi >> 1) * 8 + mr, kk * 2 + (mi & 1)));
+        for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float(&acc)[2][4] = CHAINS == 2 && (kk & 1) ? s_odd[mt] : s[mt];
-                mma16816(acc[0], qf[mt][kk], kf[0], kf[1]);
-                mma16816(acc[1], qf[mt][kk], kf[2], kf[3]);
+            for (int h = 0; h < H16; ++h) {
+                uint32_t kf[4];
+                ldsm4(kf, kst + sw<D>(16 * h + (mi >> 1) * 8 + mr, kk * 2 + (mi & 1)));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float(&acc)[NT][4] = CHAINS == 2 && (kk & 1) ? s_odd[mt] : s[mt];
+                    mma16816(acc[2 * h], qf[mt][kk], kf[0], kf[1]);
+                    mma16816(acc[2 * h + 1], qf[mt][kk], kf[2], kf[3]);
+                }
             }
-        }
+        if (CHAINS == 2)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (CHAINS == 2) s[mt][n][e] += s_odd[mt][n][e];
+                    for (int e = 0; e < 4; ++e) s[mt][n][e] += s_odd[mt][n][e];
         const int key0 = x.key * kKeys;
         if (key0 + kKeys > min_limit) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (key0 + n * 8 + c_lo + (e & 1) >= limit[mt][e >> 1])
                             s[mt][n][e] = -INFINITY;
         }
-        uint32_t pf[MT][4];
+        uint32_t pf[MT][H16][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float alpha[2];
             bool grew = false;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                float mx = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]),
-                                 fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+                float mx = fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]);
+#pragma unroll
+                for (int n = 1; n < NT; ++n) mx = fmax3(mx, s[mt][n][2 * hf], s[mt][n][2 * hf + 1]);
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float m_new = mx * p.scale_log2;
@@ -396,11 +408,13 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
                 const float neg = m[mt][hf] == -INFINITY ? 0.f : -m[mt][hf];
                 float sum = 0.f, used = 0.f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < NT; ++n) {
                     const float p0 = ex2_approx(fmaf(s[mt][n][2 * hf], p.scale_log2, neg));
                     const float p1 = ex2_approx(fmaf(s[mt][n][2 * hf + 1], p.scale_log2, neg));
+                    // weights are rounded to bf16 for the tensor cores; l_used sums them as
+                    // they are used, so that the weights applied to V add up to one
                     const uint32_t pp = pack_bf16x2(p0, p1);
-                    pf[mt][2 * n + hf] = pp;
+                    pf[mt][n >> 1][2 * (n & 1) + hf] = pp;
                     sum += p0 + p1;
                     used += __uint_as_float(pp << 16) + __uint_as_float(pp & 0xffff0000u);
                 }
@@ -418,15 +432,17 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
             }
         }
 #pragma unroll
-        for (int nn = 0; nn < D / 16; ++nn) {
-            uint32_t vf[4];
-            ldsm4_t(vf, vst + sw<D>((mi & 1) * 8 + mr, nn * 2 + (mi >> 1)));
+        for (int h = 0; h < H16; ++h)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                mma16816(o[mt][2 * nn], pf[mt], vf[0], vf[1]);
-                mma16816(o[mt][2 * nn + 1], pf[mt], vf[2], vf[3]);
+            for (int nn = 0; nn < D / 16; ++nn) {
+                uint32_t vf[4];
+                ldsm4_t(vf, vst + sw<D>(16 * h + (mi & 1) * 8 + mr, nn * 2 + (mi >> 1)));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma16816(o[mt][2 * nn], pf[mt][h], vf[0], vf[1]);
+                    mma16816(o[mt][2 * nn + 1], pf[mt][h], vf[2], vf[3]);
+                }
             }
-        }
         // ---- the piece's end: its partial result
         const bool border = x.key + 1 == x.s.groups;
         if (border || i + 1 == cnt) {
@@ -462,11 +478,13 @@ __global__ void __launch_bounds__(kWarps * 32, rows_blocks(D, MT)) kv_rows_kerne
             fresh = true;
         }
         ++x.key;
-        if (border && i + 1 < cnt) next_piece<R>(p, x);
+        if (border && i + 1 < cnt) next_piece<R, C::KEYS>(p, x);
         __syncwarp();
     }
     pdl_launch_dependents();
-    pdl_wait();  // so that this grid's end means the tile kernel's end too
+    // one block stays until the tile kernel has ended, so that the end of this grid means
+    // the end of both; the others make room for the blocks that have not started yet
+    if (blockIdx.x == 0) pdl_wait();
 }
 
 // One warp per row: its partials' log2 sums give the weights, one lane each, and the
@@ -652,27 +670,34 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // The tile kernel's share of a plan over `units` (batch rows) x H_kv heads, `tokens` tokens
 // and `keys` keys each: row blocks, and the number of key ranges that takes the least time
-// by a plain model (a wave of 148 blocks costs a range's key tiles and three more for
-// filling and draining; partials are written and read at 5 TB/s).
+// by a plain model.  A block costs its key tiles and three more for filling and draining, at
+// tile_us each; partials are written and read at 5 TB/s.  rows_bytes: what the rows kernel
+// reads beside it.  Its blocks start on every SM that the tile kernel leaves free, at some
+// 45 GB/s of keys to an SM, and take the others as they become free: so where the tile
+// kernel fits in less than a wave, fewer and longer ranges can be the better choice.
 void plan_tiles(long long units, int H_kv, int group, int tokens, int keys, int D,
-                long long part_bytes, bool joined, int& chunk, int& splits, int& blocks,
-                int& ksplit, int& parts) {
+                long long part_bytes, bool joined, double rows_bytes, int& chunk, int& splits,
+                int& blocks, int& ksplit, int& parts) {
     const int tpt = 128 / group, tiles = ceil_div(tokens, tpt);
     ksplit = tiles == 1;
     blocks = ksplit ? 1 : ceil_div(tiles, 2);
     const int kt = ceil_div(keys, 128);
     const double tile_us = (D == 128 ? 2.2 : 1.5) * (ksplit ? 0.6 : 1.0);
+    const double rows_sm_us = rows_bytes / 45e3;
     double best = 0;
     splits = 0;
     for (int s = 1; s <= kt && s <= 512; ++s) {
         const int per = ceil_div(kt, s);
         if (s > 1 && ceil_div(kt, per) != s) continue;  // the same ranges as fewer splits
-        const double waves = (double)ceil_div(units * H_kv * blocks * s, kSms);
+        const long long n = units * H_kv * blocks * s;
+        const double us = (double)ceil_div(n, kSms) * (per + 3) * tile_us;
+        const double left = rows_sm_us - (n < kSms ? (kSms - n) * us : 0.0);
         const int np = s * (1 + ksplit);
         const double join = np > 1 || joined ? 2.0 * np * part_bytes / 5e6 : 0.0;
-        const double us = waves * (per + 3) * tile_us + join + (np > 1 && !joined ? 3.0 : 0.0);
-        if (splits == 0 || us < best) {
-            best = us;
+        const double all = us + (left > 0 ? left / kSms : 0.0) + join +
+                           (np > 1 && !joined ? 3.0 : 0.0);
+        if (splits == 0 || all < best) {
+            best = all;
             splits = s;
         }
     }
@@ -701,16 +726,18 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
     long long groups = 0;  // the rows kernel's work, at most
     if (p.kind_p == kKvRows) {
         p.tiles_p = ceil_div(rows_p, R);
-        groups += (long long)ceil_div(prefix_len, kKeys) * p.tiles_p * H_kv;
+        groups += (long long)ceil_div(prefix_len, group_keys(D)) * p.tiles_p * H_kv;
     } else if (p.kind_p == kKvTiles) {
-        plan_tiles(1, H_kv, group, n_tokens, prefix_len, D, part_bytes, true, p.chunk_p,
+        // own keys beside it: somewhat over half of their bound
+        const double own = p.kind_o == kKvRows ? 0.6 * B * (double)max_len * H_kv * D * 4 : 0.0;
+        plan_tiles(1, H_kv, group, n_tokens, prefix_len, D, part_bytes, true, own, p.chunk_p,
                    p.splits_p, p.tiles_p, p.ksplit_p, p.parts_p);
     }
     if (p.kind_o == kKvRows) {
         p.tiles_o = ceil_div(rows_o, R);
-        groups += (long long)B * ceil_div(max_len, kKeys) * p.tiles_o * H_kv;
+        groups += (long long)B * ceil_div(max_len, group_keys(D)) * p.tiles_o * H_kv;
     } else {
-        plan_tiles(B, H_kv, group, max_tokens, max_len, D, part_bytes, p.kind_p != kKvNone,
+        plan_tiles(B, H_kv, group, max_tokens, max_len, D, part_bytes, p.kind_p != kKvNone, 0.0,
                    p.chunk_o, p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
     }
     p.direct = p.kind_p == kKvNone && p.kind_o == kKvTiles && p.parts_o == 1;
@@ -719,7 +746,7 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
     long long bytes = p.direct ? 0 : (p.parts_p + p.parts_o) * part_bytes;
     if (groups > 0) {
         const long long blocks = (groups + kMinGroups * kWarps - 1) / (kMinGroups * kWarps);
-        const int most = rows_blocks(D, p.mt) * kSms;
+        const int most = kBlocksPerSm * kSms;
         p.row_blocks = (int)(blocks < most ? blocks : most);
         p.j_own = p.kind_p == kKvRows ? H_kv * p.tiles_p : 0;
         const long long js =
@@ -761,7 +788,7 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
         p.slot_lse = p.slot_o + plan.slots * 16 * plan.mt * a.D;
         p.meta = (int2*)(p.slot_lse + plan.slots * 16 * plan.mt);
         const unsigned grid = (unsigned)plan.row_blocks;
-        const bool page16 = !a.tables || a.page_size % kKeys == 0;
+        const bool page16 = !a.tables || a.page_size % 16 == 0;
         if (a.D == 128) {
             if (plan.mt == 1)
                 e = page16 ? launch_rows<128, 1, true>(p, grid, tiled) : launch_rows<128, 1, false>(p, grid, tiled);

@@ -2,19 +2,22 @@
 
 Argument marshalling only: torch tensors are turned into device pointers, sizes and
 the current CUDA stream; every step of the computation runs in the library's CUDA
-kernels.  Loading fails loudly if the library has not been built -- there is no
+kernels.  The operators that run once per decoded token are marshalled by a native module
+(csrc/binding.cpp) over the same C ABI.  Loading fails loudly if the library has not been built -- there is no
 fallback path.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libra_b200.so")
+NATIVE_PATH = os.path.join(_HERE, "_ra_torch.so")
 
 RA_OK, RA_ERR_INVALID, RA_ERR_UNSUPPORTED, RA_ERR_CUDA, RA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 RA_ERR_INDEX = 5
@@ -442,68 +445,35 @@ def ring_attn_fwd(q: torch.Tensor, k_chunks, v_chunks, causal: bool, scale: floa
 
 
 # ------------------------------------------------------------------ attention over a K/V cache
-# These helpers run once per decoded token, so their checks ask a tensor for as little as
-# possible: one shape, one stride tuple, the device's index.
-_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+_native = None
 
 
-def _where(t: torch.Tensor, stream):
-    """Context in which a call on t's device allocates and launches: t's device where it is
-    not the current one, and the stream that was given (so that what is allocated here
-    belongs to the stream that uses it); None where the current ones are right."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
-                                               device=t.device)
-        return torch.cuda.stream(stream)
-    if not t.is_cuda:
-        raise ValueError("the tensors must be on a CUDA device")
-    if t.get_device() != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return None
+def native():
+    """The native binding of the cache and cross-attention entry points (_ra_torch.so, built
+    with the library): a decode step calls them once per token and layer, so their checks and
+    allocations run in C++."""
+    global _native
+    if _native is None:
+        load()
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError(f"{NATIVE_PATH} is missing: build it with "
+                               "`python -m sequence_parallelism_attn_b200.build` (no fallback path)")
+        loader = importlib.machinery.ExtensionFileLoader("_ra_torch", NATIVE_PATH)
+        spec = importlib.util.spec_from_loader("_ra_torch", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.set_error_class(RaError)
+        _native = module
+    return _native
 
 
-def _raw_stream(device: int) -> int:
-    """The current stream of a device (what torch.cuda.current_stream wraps)."""
-    return torch._C._cuda_getCurrentRawStream(device)
-
-
-def _rows(t: torch.Tensor, name: str, device: int):
-    """Shape and strides of token rows [..., H, D] whose heads are dense, on device (-1: CPU)."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != _bf16 or t.get_device() != device:
-        raise ValueError(f"{name} must be a bf16 tensor on device {device}")
-    if stride[-1] != 1 or (stride[-2] != shape[-1] and shape[-2] > 1):
-        raise ValueError(f"{name}: the heads of a token must be dense")
-    return shape, stride
-
-
-def _ints(t: torch.Tensor, name: str, device: int, shape) -> None:
-    if t.dtype != _i32 or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on device {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-
-
-def _dense(t: torch.Tensor, name: str, device: int, shape, dtype) -> None:
-    if t.dtype != dtype or t.get_device() != device or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on device "
-                         f"{device}")
-
-
-def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor, device: int):
-    """(n_pages, page_size, H_kv, D, page stride) of a cache [n_pages, page_size, H_kv, D]."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must both be [n_pages, page_size, H_kv, D]")
-    (n_pages, page_size, H_kv, D), ks = _rows(k_pages, "k_pages", device)
-    _, vs = _rows(v_pages, "v_pages", device)
-    if page_size > 1 and (ks[1] != H_kv * D or vs[1] != H_kv * D):
-        raise ValueError("the rows of a page must be dense")
-    if n_pages == 1:
-        return n_pages, page_size, H_kv, D, page_size * H_kv * D
-    if ks[0] != vs[0]:
-        raise ValueError("k_pages and v_pages must have the same page stride")
-    return n_pages, page_size, H_kv, D, ks[0]
+def _on(stream, t: torch.Tensor):
+    """The stream that was given as the current one, so that what is allocated for the call
+    belongs to the stream that uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)),
+                                           device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def paged_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -517,86 +487,13 @@ def paged_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     H_kv, D], cu_tokens int32 [B + 1], seq_lens int32 [B] (the new tokens included),
     block_tables int32 [B, max_pages], inv_freq fp32 [rot_dim / 2] (None: no rotation).
     Returns the rotated q [N, H_q, D] (q_out, which may be q itself), or None without q."""
-    ctx = _where(k, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None:
+        with _on(stream, k):
             return paged_kv_append(q, k, v, k_pages, v_pages, cu_tokens, seq_lens, block_tables,
                                    inv_freq, max_tokens, pos_offset, interleaved, q_out)
-    dev = k.get_device()
-    n_pages, page_size, H_kv, D, page_stride = _cache(k_pages, v_pages, dev)
-    shape, ks = _rows(k, "k", dev)
-    N = shape[0]
-    if shape != (N, H_kv, D) or v.shape != shape:
-        raise ValueError("k and v must be [N, H_kv, D] with the cache's heads")
-    _, vs = _rows(v, "v", dev)
-    B, max_pages = block_tables.shape
-    _ints(cu_tokens, "cu_tokens", dev, (B + 1,))
-    _ints(seq_lens, "seq_lens", dev, (B,))
-    _ints(block_tables, "block_tables", dev, (B, max_pages))
-    rot, inv_ptr = 0, None
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _dense(inv_freq, "inv_freq", dev, (rot // 2,), _f32)
-        inv_ptr = inv_freq.data_ptr()
-    H_q = q_ptr = q_ts = qo_ptr = qo_ts = 0
-    if q is not None:
-        shape, qs = _rows(q, "q", dev)
-        H_q = shape[1]
-        if shape != (N, H_q, D):
-            raise ValueError("q must be [N, H_q, D]")
-        dense = H_q * D
-        q_ptr, q_ts, qo_ts = q.data_ptr(), qs[0] if N > 1 else dense, dense
-        if q_out is None:
-            q_out = q.new_empty(shape)
-        else:
-            got, os = _rows(q_out, "q_out", dev)
-            if got != shape:
-                raise ValueError("q_out must have q's shape")
-            if N > 1:
-                qo_ts = os[0]
-        qo_ptr = q_out.data_ptr()
-    dense = H_kv * D
-    _check((_lib or load()).ra_paged_kv_append(
-        q_ptr, k.data_ptr(), v.data_ptr(), q_ts, ks[0] if N > 1 else dense,
-        vs[0] if N > 1 else dense, cu_tokens.data_ptr(), seq_lens.data_ptr(),
-        block_tables.data_ptr(), inv_ptr, B, N, max_tokens if max_tokens < N else N, H_q, H_kv, D,
-        rot, 1 if interleaved else 0, pos_offset, page_size, n_pages, max_pages, page_stride,
-        RA_BF16, qo_ptr, qo_ts, k_pages.data_ptr(), v_pages.data_ptr(), _raw_stream(dev)))
-    return q_out if q is not None else None
-
-
-@functools.lru_cache(maxsize=4096)
-def _prefix_workspace(*sizes: int) -> int:
-    return load().ra_prefix_attn_workspace(*sizes)
-
-
-@functools.lru_cache(maxsize=4096)
-def _cross_workspace(*sizes: int) -> int:
-    return load().ra_cross_attn_workspace(*sizes)
-
-
-def _workspace(need: int, workspace: torch.Tensor | None, like: torch.Tensor, device: int):
-    """(pointer, bytes, tensor) of the caller's workspace, or of a new one."""
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = like.new_empty((need + 1) // 2)  # bf16 elements
-    elif workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on device {device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _results(q: torch.Tensor, shape, lse_shape, out_dtype, out, lse, device: int):
-    """The outputs that were given, checked, or new ones."""
-    if out is None:
-        out = q.new_empty(shape, dtype=out_dtype)
-    else:
-        _dense(out, "out", device, shape, out.dtype)
-    if lse is None:
-        lse = q.new_empty(lse_shape, dtype=_f32)
-    else:
-        _dense(lse, "lse", device, lse_shape, _f32)
-    return out, lse, _dt(out.dtype)
+    return (_native or native()).paged_kv_append(
+        q, k, v, k_pages, v_pages, cu_tokens, seq_lens, block_tables, inv_freq, max_tokens,
+        pos_offset, interleaved, q_out)
 
 
 def prefix_attn_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -614,61 +511,14 @@ def prefix_attn_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     plain paged attention.  Rows past cu_tokens[B] are not written.  Returns
     (out [N, H_q, D] in out_dtype, lse [H_q, N] fp32); the workspace
     (ra_prefix_attn_workspace bytes) is allocated here when not given."""
-    ctx = _where(q, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None:
+        with _on(stream, q):
             return prefix_attn_fwd(q, k_pages, v_pages, cu_tokens, seq_lens, block_tables,
                                    max_tokens, max_len, prefix_table, prefix_len, scale,
                                    out_dtype, out, lse, workspace)
-    dev = q.get_device()
-    n_pages, page_size, H_kv, D, page_stride = _cache(k_pages, v_pages, dev)
-    shape, qs = _rows(q, "q", dev)
-    N, H_q, Dq = shape
-    if Dq != D:
-        raise ValueError("q and the cache must have the same head dimension")
-    B, max_pages = block_tables.shape
-    _ints(cu_tokens, "cu_tokens", dev, (B + 1,))
-    _ints(seq_lens, "seq_lens", dev, (B,))
-    _ints(block_tables, "block_tables", dev, (B, max_pages))
-    table = None
-    if prefix_len > 0:
-        if prefix_table is None or prefix_table.numel() * page_size < prefix_len:
-            raise ValueError("prefix_table must name ceil(prefix_len / page_size) pages")
-        _ints(prefix_table, "prefix_table", dev, (prefix_table.numel(),))
-        table = prefix_table.data_ptr()
-    if max_len is None:
-        max_len = max_pages * page_size
-    if max_tokens > N:
-        max_tokens = N
-    if scale is None:
-        scale = D ** -0.5
-    out, lse, out_dt = _results(q, shape, (H_q, N), out_dtype, out, lse, dev)
-    ws, ws_bytes, keep = _workspace(
-        _prefix_workspace(B, N, max_tokens, max_len, prefix_len, H_q, H_kv, D, page_size),
-        workspace, q, dev)
-    _check((_lib or load()).ra_prefix_attn_fwd(
-        q.data_ptr(), qs[0] if N > 1 else H_q * D, k_pages.data_ptr(), v_pages.data_ptr(),
-        cu_tokens.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(), table, prefix_len, B,
-        N, max_tokens, max_len, H_q, H_kv, D, page_size, n_pages, max_pages, page_stride, scale,
-        RA_BF16, out_dt, out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _raw_stream(dev)))
-    return out, lse
-
-
-def _cross_strides(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, device: int):
-    """Checked sizes and strides of cross attention's inputs."""
-    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape:
-        raise ValueError("q must be [B, Lq, H_q, D], k and v [B, Lk, H_kv, D]")
-    (B, Lq, H_q, D), qs = _rows(q, "q", device)
-    (Bk, Lk, H_kv, Dk), ks = _rows(k, "k", device)
-    _, vs = _rows(v, "v", device)
-    if Bk != B or Dk != D:
-        raise ValueError("q, k and v must have the same batch and head dimension")
-    # the stride of a dimension with one entry says nothing: the dense one in its place
-    qt, kt = (qs[1] if Lq > 1 else H_q * D), (ks[1] if Lk > 1 else H_kv * D)
-    qb, kb = (qs[0], ks[0]) if B > 1 else (Lq * qt, Lk * kt)
-    if (Lk > 1 and vs[1] != kt) or (B > 1 and vs[0] != kb):
-        raise ValueError("k and v must have the same strides")
-    return B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb
+    return (_native or native()).prefix_attn_fwd(
+        q, k_pages, v_pages, cu_tokens, seq_lens, block_tables, max_tokens, max_len, prefix_table,
+        prefix_len, scale, out_dtype, out, lse, workspace)
 
 
 def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -680,24 +530,11 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     tokens and batch rows may be strided, k and v alike), per batch row the first kv_lens[b]
     of them (int32 [B]; None: all) (ra_cross_attn_fwd).  Returns (out [B, Lq, H_q, D] in
     out_dtype, lse [B, H_q, Lq] fp32)."""
-    ctx = _where(q, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None:
+        with _on(stream, q):
             return cross_attn_fwd(q, k, v, kv_lens, scale, out_dtype, out, lse, workspace)
-    dev = q.get_device()
-    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v, dev)
-    lens = None
-    if kv_lens is not None:
-        _ints(kv_lens, "kv_lens", dev, (B,))
-        lens = kv_lens.data_ptr()
-    if scale is None:
-        scale = D ** -0.5
-    out, lse, out_dt = _results(q, (B, Lq, H_q, D), (B, H_q, Lq), out_dtype, out, lse, dev)
-    ws, ws_bytes, keep = _workspace(_cross_workspace(B, Lq, Lk, H_q, H_kv, D), workspace, q, dev)
-    _check((_lib or load()).ra_cross_attn_fwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb,
-        scale, RA_BF16, out_dt, out.data_ptr(), lse.data_ptr(), ws, ws_bytes, _raw_stream(dev)))
-    return out, lse
+    return (_native or native()).cross_attn_fwd(q, k, v, kv_lens, scale, out_dtype, out, lse,
+                                                workspace)
 
 
 def cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -708,31 +545,8 @@ def cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch
     it, out (bf16) and lse its results, dout [B, Lq, H_q, D] bf16.  Returns dq
     [B, Lq, H_q, D], dk, dv [B, Lk, H_kv, D] in grad_dtype (fp32 or bf16), zero past
     kv_lens[b]."""
-    ctx = _where(q, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None:
+        with _on(stream, q):
             return cross_attn_bwd(q, k, v, out, lse, dout, kv_lens, scale, grad_dtype, workspace)
-    dev = q.get_device()
-    B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb = _cross_strides(q, k, v, dev)
-    lens = None
-    if kv_lens is not None:
-        _ints(kv_lens, "kv_lens", dev, (B,))
-        lens = kv_lens.data_ptr()
-    shape = (B, Lq, H_q, D)
-    _dense(out, "out", dev, shape, _bf16)
-    _dense(dout, "dout", dev, shape, _bf16)
-    _dense(lse, "lse", dev, (B, H_q, Lq), _f32)
-    if scale is None:
-        scale = D ** -0.5
-    dq = q.new_empty(shape, dtype=grad_dtype)
-    dk = q.new_empty((B, Lk, H_kv, D), dtype=grad_dtype)
-    dv = q.new_empty((B, Lk, H_kv, D), dtype=grad_dtype)
-    lib = _lib or load()
-    gd = _dt(grad_dtype)
-    ws, ws_bytes, keep = _workspace(lib.ra_cross_attn_bwd_workspace(B, Lq, H_q, D, gd), workspace,
-                                    q, dev)
-    _check(lib.ra_cross_attn_bwd(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), lens, out.data_ptr(), lse.data_ptr(),
-        dout.data_ptr(), B, Lq, Lk, H_q, H_kv, D, qt, qb, kt, kb, scale, RA_BF16, gd,
-        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws, ws_bytes, _raw_stream(dev)))
-    return dq, dk, dv
+    return (_native or native()).cross_attn_bwd(q, k, v, out, lse, dout, kv_lens, scale,
+                                                grad_dtype, workspace)

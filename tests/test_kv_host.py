@@ -87,32 +87,41 @@ def test_workspace_sizes(lib):
 
 
 def test_binding_refusals():
-    """The Python helpers check shapes, types and layouts before the library is called."""
+    """The binding checks shapes, types and layouts before the library is called."""
     from sequence_parallelism_attn_b200 import ra
+    nat = ra.native()
     bf = dict(dtype=torch.bfloat16)
-    dev = -1  # the CPU
     pages = torch.zeros(4, 16, 2, 64, **bf)
-    with pytest.raises(ValueError):
-        ra._cache(pages, pages[:, :8], dev)
-    with pytest.raises(ValueError):
-        ra._cache(pages.float(), pages.float(), dev)
-    with pytest.raises(ValueError):
-        ra._cache(pages, torch.zeros(4, 2, 16, 2, 64, **bf)[:, 0], dev)
     inter = torch.zeros(4, 2, 16, 2, 64, **bf)
-    assert ra._cache(inter[:, 0], inter[:, 1], dev) == (4, 16, 2, 64, 4096)
-    with pytest.raises(ValueError):
-        ra._ints(torch.zeros(3, dtype=torch.int64), "x", dev, (3,))
-    with pytest.raises(ValueError):
-        ra._ints(torch.zeros(3, dtype=torch.int32), "x", dev, (4,))
-    with pytest.raises(ValueError):
-        ra.cross_attn_fwd(*(torch.zeros(2, 5, 4, 64, **bf),) * 3)  # not on a GPU
+    assert nat.check_cache(inter[:, 0], inter[:, 1]) == (4, 16, 2, 64, 4096)
+    assert nat.check_cache(pages[:1], pages[:1]) == (1, 16, 2, 64, 2048)
+    for bad in ((pages, pages[:, :8]), (pages.float(), pages.float()), (pages, inter[:, 0]),
+                (pages[..., ::2], pages[..., ::2]), (pages[:, :, :1], pages[:, :, :1]),
+                (pages[0], pages[0])):
+        with pytest.raises(ValueError):
+            nat.check_cache(*bad)
+    i32 = dict(dtype=torch.int32)
+    cu, lens, tables = torch.zeros(4, **i32), torch.zeros(3, **i32), torch.zeros(3, 5, **i32)
+    assert nat.check_batch(cu, lens, tables) == (3, 5)
+    for bad in ((cu.long(), lens, tables), (cu[:3], lens, tables), (cu, lens[:2], tables),
+                (cu, lens, tables[:, 0]), (cu, lens, tables[:, ::2]), (cu, lens.float(), tables)):
+        with pytest.raises(ValueError):
+            nat.check_batch(*bad)
     q, k = torch.zeros(2, 5, 4, 64, **bf), torch.zeros(2, 7, 2, 64, **bf)
-    assert ra._cross_strides(q, k, k, dev) == (2, 5, 7, 4, 2, 64, 256, 1280, 128, 896)
+    assert nat.check_cross(q, k, k, None) == (2, 5, 7, 4, 2, 64, 256, 1280, 128, 896)
+    kv = torch.zeros(2, 7, 2, 2, 64, **bf)
+    assert nat.check_cross(q, kv[:, :, 0], kv[:, :, 1], torch.zeros(2, **i32))[8:] == (256, 1792)
     for bad in ((q, k[:1], k[:1]), (q, k[..., :32], k[..., :32]), (q, k, k[:, :6]),
                 (q.float(), k, k), (q.transpose(1, 2), k, k),
                 (q, k, torch.zeros(2, 7, 4, 64, **bf)[:, :, :2])):
         with pytest.raises(ValueError):
-            ra._cross_strides(*bad, dev)
+            nat.check_cross(*bad, None)
+    with pytest.raises(ValueError):
+        nat.check_cross(q, k, k, torch.zeros(3, **i32))
+    with pytest.raises(ValueError):
+        ra.cross_attn_fwd(q, k, k)  # not on a GPU
+    with pytest.raises(ValueError):
+        ra.paged_kv_append(q[0], k[0], k[0], pages, pages, cu, lens, tables, None, 1)
 
 
 CROSS_BWD = dict(q=FAKE, k=FAKE, v=FAKE, lens=FAKE, o=FAKE, lse=FAKE, do=FAKE, B=2, Lq=3, Lk=50,
