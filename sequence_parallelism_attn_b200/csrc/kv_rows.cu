@@ -34,7 +34,7 @@ constexpr int kWarps = 4;
 // Keys of a group: 8 KB of K and V either way.  At D = 64 a group of 16 spent as much on the
 // softmax's latencies as on its bytes (5.5 TB/s in the long run, against 6.2 at D = 128).
 constexpr int group_keys(int D) { return D == 64 ? 32 : 16; }
-constexpr int kMinGroups = 4;  // fewest groups of a warp's stretch
+constexpr int kMinGroups = 2;  // fewest groups of a warp's stretch (1, 2, 4: 10.7, 10.0, 10.9 us a small call)
 constexpr float kRescale = 8.0f;  // log2 units: the maximum may lag by 2^8
 
 struct RowsParams {

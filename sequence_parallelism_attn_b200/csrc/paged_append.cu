@@ -59,6 +59,29 @@ __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ App
     if (threadIdx.x == 0 && t0 == 0 && n > a.max_tokens) atomicOr(&g_append_error_word, kKvErrTokens);
     const int nt = min(n - t0, kTokens);
     if (nt <= 0) return;
+    // a unit's vectors, loaded before the places and angles are worked out
+    const int units = (a.H_q + 2 * a.H_kv) * UPH, ru = a.rot / 16;
+    uint4 x[kTokens], y[kTokens];
+    int v0 = 0, v1 = 0;
+    auto load = [&](int u) {
+        const int head = u / UPH, j = u % UPH;
+        const bool is_q = head < a.H_q, is_v = head >= a.H_q + a.H_kv;
+        const int h = is_q ? head : (is_v ? head - a.H_q - a.H_kv : head - a.H_q);
+        const uint16_t* src = (const uint16_t*)(is_q ? a.q : (is_v ? a.v : a.k));
+        const long long stride = is_q ? a.q_tstride : (is_v ? a.v_tstride : a.k_tstride);
+        const bool halves = !a.interleaved && j < ru;  // the two halves of 8 rotated pairs
+        v0 = halves ? j : 2 * j;
+        v1 = halves ? j + ru : 2 * j + 1;
+#pragma unroll
+        for (int t = 0; t < kTokens; ++t)
+            if (t < nt) {
+                const uint4* r =
+                    reinterpret_cast<const uint4*>(src + (long long)(c0 + t0 + t) * stride + h * D);
+                x[t] = r[v0];
+                y[t] = r[v1];
+            }
+    };
+    if (threadIdx.x < units) load(threadIdx.x);
     if (threadIdx.x < nt) {
         const int pos = len - n + t0 + (int)threadIdx.x;
         long long off = -1;
@@ -90,29 +113,12 @@ __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ App
         cs[t][j] = make_float2(c, s);
     }
     __syncthreads();
-    const int units = (a.H_q + 2 * a.H_kv) * UPH;
-    const int ru = a.rot / 16;
     for (int u = threadIdx.x; u < units; u += blockDim.x) {
+        if (u >= blockDim.x) load(u);
         const int head = u / UPH, j = u % UPH;
         const bool is_q = head < a.H_q, is_v = head >= a.H_q + a.H_kv;
         const int h = is_q ? head : (is_v ? head - a.H_q - a.H_kv : head - a.H_q);
-        const uint16_t* src = (const uint16_t*)(is_q ? a.q : (is_v ? a.v : a.k));
-        const long long stride = is_q ? a.q_tstride : (is_v ? a.v_tstride : a.k_tstride);
         const bool turned = !is_v && j < ru;
-        int v0 = 2 * j, v1 = 2 * j + 1;  // the two vectors of the head
-        if (!a.interleaved && j < ru) {
-            v0 = j;
-            v1 = j + ru;
-        }
-        uint4 x[kTokens], y[kTokens];
-#pragma unroll
-        for (int t = 0; t < kTokens; ++t)
-            if (t < nt) {
-                const uint4* r =
-                    reinterpret_cast<const uint4*>(src + (long long)(c0 + t0 + t) * stride + h * D);
-                x[t] = r[v0];
-                y[t] = r[v1];
-            }
 #pragma unroll
         for (int t = 0; t < kTokens; ++t)
             if (t < nt) {
