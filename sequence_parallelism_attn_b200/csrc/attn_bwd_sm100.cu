@@ -852,6 +852,7 @@ struct BCfg {
     static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
     static_assert(COL_DK + D <= kTmemCols, "tensor memory budget");
     static_assert(D <= 128, "dQ of one item fits in the dP^T region");
+    static_assert(2 * 128 * (D * 4 + 16) <= OFF_DS, "cross: the gradients' stage");
 };
 
 template <int D, int LAYOUT, bool SKIP_DQ>
@@ -1365,36 +1366,37 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
             const int which = c;  // warpgroup 0 writes dV, warpgroup 1 dK (times scale)
             const float mul = which ? p.scale : 1.f;
             float* outp = which ? p.dk[j] : p.dv[j];
+            const uint32_t row_bytes = p.grad_bf16 ? D * 2 : D * 4;  // cross
+            const uint32_t stg_row = base + C::OFF_A + (uint32_t)(which * 128 + key_t) * (row_bytes + 16);
 #pragma unroll
             for (int cb = 0; cb < D / 32; ++cb) {
                 uint32_t o[32];
                 tmem_ld32(tmem + lane_off + C::COL_DV + which * D + cb * 32, o);
                 tmem_wait_ld();
                 if (CROSS) {
-                    // every row of the states is written, zeros past the batch row's keys
-                    if (t * kBN + key_t < p.Lc) {
-                        const float m = key_ok ? mul : 0.f;
-                        if (p.grad_bf16) {
-                            uint4* dst = reinterpret_cast<uint4*>(
-                                reinterpret_cast<uint16_t*>(outp) + orow + cb * 32);
+                    // every row of the states is written, zeros past the batch row's keys:
+                    // staged in shared memory, one bulk copy per row (the threads' own
+                    // stores, 16 bytes of 32 rows at a time, took 2 us more a tile).  Every
+                    // MMA has completed (acc_done), so K, V and the ring hold the stage.
+                    const float m = key_ok ? mul : 0.f;
+                    if (p.grad_bf16) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t w[4];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * m,
-                                                       __uint_as_float(o[8 * i + 2 * e + 1]) * m);
-                                dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-                            float4* dst = reinterpret_cast<float4*>(outp + orow + cb * 32);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                dst[i] = make_float4(__uint_as_float(o[4 * i]) * m,
-                                                     __uint_as_float(o[4 * i + 1]) * m,
-                                                     __uint_as_float(o[4 * i + 2]) * m,
-                                                     __uint_as_float(o[4 * i + 3]) * m);
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * m,
+                                                   __uint_as_float(o[8 * i + 2 * e + 1]) * m);
+                            st_shared_v4(stg_row + cb * 64 + i * 16, w[0], w[1], w[2], w[3]);
                         }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            st_shared_v4(stg_row + cb * 128 + i * 16,
+                                         __float_as_uint(__uint_as_float(o[4 * i]) * m),
+                                         __float_as_uint(__uint_as_float(o[4 * i + 1]) * m),
+                                         __float_as_uint(__uint_as_float(o[4 * i + 2]) * m),
+                                         __float_as_uint(__uint_as_float(o[4 * i + 3]) * m));
                     }
                     continue;
                 }
@@ -1416,6 +1418,15 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
                         dst[i] = r;
                     }
                 }
+            }
+            if (CROSS) {
+                fence_proxy_async_smem();
+                if (t * kBN + key_t < p.Lc) {
+                    bulk_store(reinterpret_cast<uint8_t*>(outp) + orow * (p.grad_bf16 ? 2 : 4),
+                               stg_row, row_bytes);
+                    bulk_commit();
+                }
+                bulk_wait_all();
             }
         } else if (CROSS && ok && n == 0) {  // past the batch row's keys
             if (t * kBN + key_t < p.Lc) {

@@ -102,6 +102,14 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                  "r"(d)
                  : "memory");
 }
+// Plain bulk store shared -> global (bulk-group completion): both addresses 16-byte aligned,
+// the size a multiple of 16.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                     reinterpret_cast<uint64_t>(dst)),
+                 "r"(src), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -303,6 +311,23 @@ __device__ __forceinline__ uint32_t softmax_pair(uint64_t s2, uint64_t scale2, u
     return pp;
 }
 
+
+// The same without the sum of the bf16 values (a quarter of the step's instructions).
+__device__ __forceinline__ uint32_t softmax_pair_fp32(uint64_t s2, uint64_t scale2, uint64_t negm2,
+                                                      uint64_t& sum) {
+    uint32_t pp;
+    asm("{\n\t.reg .b32 x0, x1, p0, p1;\n\t.reg .b64 x, p;\n\t"
+        "fma.rn.f32x2 x, %2, %3, %4;\n\t"
+        "mov.b64 {x0, x1}, x;\n\t"
+        "ex2.approx.ftz.f32 p0, x0;\n\t"
+        "ex2.approx.ftz.f32 p1, x1;\n\t"
+        "cvt.rn.bf16x2.f32 %0, p1, p0;\n\t"
+        "mov.b64 p, {p0, p1};\n\t"
+        "add.rn.f32x2 %1, %1, p;\n\t}"
+        : "=r"(pp), "+l"(sum)
+        : "l"(s2), "l"(scale2), "l"(negm2));
+    return pp;
+}
 
 // ------------------------------------------------------------------ register split
 // Per-warpgroup register budget change (all 4 warps of the warpgroup execute it).  The
