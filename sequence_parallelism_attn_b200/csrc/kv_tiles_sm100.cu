@@ -406,6 +406,7 @@ __device__ __forceinline__ void softmax_wg(const TileParams& p, uint32_t base, u
     const int tile_t0 = x.t0 + (x.ksplit ? 0 : wg * p.tpt);
     const int t = tile_t0 + tl;
     const bool row_ok = tl < p.tpt && t < x.n_tok;
+    const bool live = __any_sync(FULL, row_ok);
     // keys below `limit` are seen; the tile's smallest limit is its first token's
     const int limit = x.causal && row_ok ? min(x.k_hi, x.lim0 + t) : x.k_hi;
     const int limit_min = x.causal ? min(x.k_hi, x.lim0 + tile_t0) : x.k_hi;
@@ -429,6 +430,21 @@ __device__ __forceinline__ void softmax_wg(const TileParams& p, uint32_t base, u
             break;
         }
         __syncwarp();
+        if (!live) {
+            // none of the warp's rows is a token's: it keeps the barriers' count and leaves
+            // the exponentials to the others (its rows of P and O are never read).  Waiting
+            // for PV(i-1) keeps its arrival out of the phase before.
+            tc_fence_before();
+            mbar_arrive(bar(C::bar_sfree(wg)));
+            if (i > 0 &&
+                !wait_warp(bar(C::bar_pvd(wg)), (i - 1) & 1, abort_flag, lim, kErrSoftmax)) {
+                ok = false;
+                break;
+            }
+            __syncwarp();
+            mbar_arrive(bar(C::bar_pf(wg)));
+            continue;
+        }
         tc_fence_after();
         uint64_t s2[64];  // the row's 128 scores as pairs (2i, 2i+1)
         tmem_ld128_pairs(tS, s2);

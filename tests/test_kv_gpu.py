@@ -79,6 +79,16 @@ PREFIX = [  # n, lens, page, hq, hkv, d, prefix
     ([140], [141], 128, 1, 1, 128, 127),
     ([3, 2], [30, 9], 16, 48, 1, 64, 50),                     # 48 heads per kv head
     ([2, 1], [30, 9], 16, 130, 1, 64, 50),                    # more than a row tile's
+    ([5, 3], [40, 100], 16, 4, 1, 64, 0),                     # row tiles of 32
+    ([4, 4], [4, 100], 16, 4, 1, 128, 20),
+    ([40, 7], [90, 50], 5, 4, 1, 128, 31),                    # many row tiles of odd pages
+    ([1], [5000], 64, 2, 1, 64, 0),                           # one sequence for all warps
+    ([1], [3000], 64, 8, 1, 128, 2500),
+    # several scans of 32 sequences, with sequences without tokens and without keys
+    ([(7 * i) % 3 for i in range(75)], [(7 * i) % 3 * (1 + 13 * i % 50) for i in range(75)], 16,
+     4, 2, 64, 19),
+    ([1] * 100, [1 + 37 * i % 90 for i in range(100)], 16, 2, 2, 128, 0),
+    ([0] * 40 + [1], [0] * 40 + [33], 16, 2, 1, 64, 0),
 ]
 
 
@@ -292,6 +302,9 @@ CROSS = [  # B, Lq, Lk, lens, hq, hkv, d
     (1, 40, 1100, [1029], 1, 1, 128),
     (2, 500, 64, [64, 63], 8, 2, 64),
     (1, 129, 2000, None, 2, 1, 64),
+    (70, 1, 90, [(11 * b) % 91 for b in range(70)], 4, 2, 64),
+    (40, 2, 200, [(50 * b) % 201 for b in range(40)], 2, 1, 128),
+    (1, 1, 6000, [5999], 4, 1, 64),
 ]
 
 
