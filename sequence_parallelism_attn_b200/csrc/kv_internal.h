@@ -59,6 +59,7 @@ struct KvPlan {
     int kind_o, chunk_o, splits_o, tiles_o, ksplit_o, parts_o;  // own keys
     int mt;                       // rows kernel: 16-row fragments of a row tile
     int row_blocks, j_own;        // its grid; index of the first (sequence, head, tile)
+    int min_groups, wide_combine; // fewest key groups of a warp; eight warps join a row
     long long slots;              // its partial slots
     int direct;                   // a single part: results written without partials
     long long blocks, workspace;  // largest index of a launch (to be below 2^31), bytes

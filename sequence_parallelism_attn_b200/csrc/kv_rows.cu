@@ -34,7 +34,6 @@ constexpr int kWarps = 4;
 // Keys of a group: 8 KB of K and V either way.  At D = 64 a group of 16 spent as much on the
 // softmax's latencies as on its bytes (5.5 TB/s in the long run, against 6.2 at D = 128).
 constexpr int group_keys(int D) { return D == 64 ? 32 : 16; }
-constexpr int kMinGroups = 2;  // fewest groups of a warp's stretch (1, 2, 4: 10.7, 10.0, 10.9 us a small call)
 constexpr float kRescale = 8.0f;  // log2 units: the maximum may lag by 2^8
 
 struct RowsParams {
@@ -181,7 +180,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
         unsigned mine = w_first;
         for (int b0 = 32; b0 < a.B; b0 += 32) mine += weight(b0 + lane);
         const unsigned total = (w_prefix + __reduce_add_sync(0xffffffffu, mine)) * a.H_kv;
-        per = max((total + n_warps - 1) / n_warps, (unsigned)kMinGroups);
+        per = max((total + n_warps - 1) / n_warps, (unsigned)p.p.min_groups);
         // (a stretch that starts past the end is empty; the product may wrap there)
         const bool some = wid < (int)((total + per - 1) / per);
         f0 = per * wid;
@@ -490,12 +489,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
 // One warp per row: its partials' log2 sums give the weights, one lane each, and the
 // weighted outputs are added up in the splits' order (the same bits on every call), 16 bytes
 // a lane: whole rows of D = 128, two partials at a time of D = 64.  It lives on latency (a
-// row's partials are some KB in L2), so eight partials' loads are in flight at once.
-template <int D>
+// row's partials are some KB in L2), so eight partials' loads are in flight at once.  Where
+// few rows have many partials each (WPR = 8), a block's eight warps share a row's partials
+// and merge their sums: 2 sequences of 16 rows behind 11705 keys, 366 partials to a row,
+// took 55 us with one warp to a row.
+template <int D, int WPR>
 __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__ RowsParams p) {
     const KvArgs& a = p.a;
-    const int idx = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5);  // below 2^31 + 8: checked
-    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int idx = WPR == 8 ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;  // < 2^31 + 8
     const long long rows = (long long)a.n_tokens * a.H_q;
     const int R = 16 * p.p.mt;
     // the row: by token, or by (sequence, its token) where the rows kernel took the own keys
@@ -564,11 +566,13 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         o2 = p.slot_o + ((long long)mt.x * R + r % R) * D;
         l2 = p.slot_lse + (long long)mt.x * R + r % R;
     }
-    const int ns = n1 + n2;
+    // this warp's partials: [from, ns)
+    const int all = n1 + n2, share = (all + WPR - 1) / WPR;
+    const int from = WPR == 8 ? warp * share : 0, ns = WPR == 8 ? min(from + share, all) : all;
     auto lse_of = [&](int s) { return s < n1 ? l1[s * s1] : l2[(s - n1) * s2]; };
-    const float first = lane < ns ? lse_of(lane) : -INFINITY;
+    const float first = from + lane < ns ? lse_of(from + lane) : -INFINITY;
     float mm = first;
-    for (int s = lane + 32; s < ns; s += 32) mm = fmaxf(mm, lse_of(s));
+    for (int s = from + lane + 32; s < ns; s += 32) mm = fmaxf(mm, lse_of(s));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
     const float ms = mm == -INFINITY ? 0.f : mm;  // (a NaN partial comes through as NaN)
@@ -577,8 +581,8 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     const int sub = lane / LPR, c = (lane % LPR) * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    for (int base = 0; base < ns; base += 32) {
-        const float x = base == 0 ? first
+    for (int base = from; base < ns; base += 32) {
+        const float x = base == from ? first
                         : base + lane < ns ? lse_of(base + lane) : -INFINITY;
         const float w = ex2_approx(x - ms);
         sum += w;
@@ -615,6 +619,35 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
         acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
     }
+    float top = ms;  // what the weights are relative to
+    if (WPR == 8) {
+        __shared__ float4 s_acc[8][LPR];
+        __shared__ float s_m[8], s_sum[8];
+        if (sub == 0) s_acc[warp][c / 4] = acc;
+        if (lane == 0) {
+            s_m[warp] = mm;
+            s_sum[warp] = sum;
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        float m8 = s_m[0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) m8 = fmaxf(m8, s_m[w]);
+        top = m8 == -INFINITY ? 0.f : m8;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            // a warp without a finite maximum summed relative to 0 (nothing, or a NaN)
+            const float f = s_m[w] == -INFINITY ? 1.f : ex2_approx(s_m[w] - top);
+            const float4 v = s_acc[w][c / 4];
+            sum = fmaf(f, s_sum[w], sum);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+        }
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (sub == 0) {
         if (a.out_bf16)
@@ -633,7 +666,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
             const int bb = fdiv(tok, p.dtokens), tt = tok - bb * a.max_tokens;
             li = ((long long)bb * a.H_q + head) * a.max_tokens + tt;
         }
-        a.lse[li] = sum == 0.f ? -INFINITY : (ms + log2f(sum)) * 0.69314718055994530942f;
+        a.lse[li] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
     }
 }
 
@@ -745,9 +778,22 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
                (p.kind_o == kKvTiles ? (long long)B * p.splits_o * H_kv * p.tiles_o : 0);
     long long bytes = p.direct ? 0 : (p.parts_p + p.parts_o) * part_bytes;
     if (groups > 0) {
-        const long long blocks = (groups + kMinGroups * kWarps - 1) / (kMinGroups * kWarps);
+        // A stretch costs its groups, every partial of a row some of the combine's time: with
+        // G groups in the longest run of keys, about sqrt(G / 16) groups are the least worth
+        // a warp (1, 2, 4 groups, a call of 1000 + 300 keys: 10.7, 10.0, 10.9 us).
+        const int longest = ceil_div(p.kind_p == kKvRows && prefix_len > max_len ? prefix_len
+                                                                                 : max_len,
+                                     group_keys(D));
+        p.min_groups = 2;
+        while ((p.min_groups + 1) * (p.min_groups + 1) * 16 <= longest && p.min_groups < 16)
+            ++p.min_groups;
+        const long long least = (long long)p.min_groups * kWarps;
+        const long long blocks = (groups + least - 1) / least;
         const int most = kBlocksPerSm * kSms;
         p.row_blocks = (int)(blocks < most ? blocks : most);
+        long long per = groups / (p.row_blocks * kWarps);  // of a full batch
+        if (per < p.min_groups) per = p.min_groups;
+        p.wide_combine = longest / per + p.parts_p > 16;
         p.j_own = p.kind_p == kKvRows ? H_kv * p.tiles_p : 0;
         const long long js =
             p.j_own + (p.kind_o == kKvRows ? (long long)B * H_kv * p.tiles_o : 0);
@@ -804,9 +850,14 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
     if (e != cudaSuccess || plan.direct) return e;
     const long long out_rows =
         plan.kind_o == kKvRows ? (long long)a.B * a.max_tokens * a.H_q : rows;
+    if (plan.wide_combine) {
+        const unsigned cg = (unsigned)out_rows;
+        return a.D == 128 ? launch_pdl(kv_combine_kernel<128, 8>, p, cg, 256, 0, a.stream, true)
+                          : launch_pdl(kv_combine_kernel<64, 8>, p, cg, 256, 0, a.stream, true);
+    }
     const unsigned cg = (unsigned)((out_rows + 7) / 8);
-    return a.D == 128 ? launch_pdl(kv_combine_kernel<128>, p, cg, 256, 0, a.stream, true)
-                      : launch_pdl(kv_combine_kernel<64>, p, cg, 256, 0, a.stream, true);
+    return a.D == 128 ? launch_pdl(kv_combine_kernel<128, 1>, p, cg, 256, 0, a.stream, true)
+                      : launch_pdl(kv_combine_kernel<64, 1>, p, cg, 256, 0, a.stream, true);
 }
 
 cudaError_t read_and_clear_kv_error(unsigned int* value) {
