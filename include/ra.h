@@ -435,7 +435,8 @@ RA_API ra_status ra_ulysses_head2seq_grouped(const void* in, void* out, int P, i
  *   - block_tables: device int32, [B][max_pages]: key j of sequence b is row j % page_size of
  *     page block_tables[b][j / page_size].  Entries past a sequence's length are not read.
  *   - The device arrays may change between launches of a captured graph; host arguments are
- *     bounds and stay.
+ *     bounds and stay.  The first call of a kind in a process loads its kernels: make it
+ *     before a capture.
  *   - Device values outside their bounds (n_b > max_tokens, seq_lens[b] > max_len or < n_b
  *     for the append, a page id outside [0, n_pages)) are never followed: the kernel skips
  *     or clamps them, what it writes for that sequence is undefined, and ra_sync_status()

@@ -21,6 +21,7 @@
 // 16-row fragments (a tcgen05 tile has at least 64 rows) and the deep per-warp rings.
 #include <cuda_bf16.h>
 #include <cmath>
+#include <cstring>
 #include "kv_internal.h"
 #include "sm100_ptx.cuh"
 
@@ -702,12 +703,17 @@ cudaError_t launch_rows(const RowsParams& p, unsigned grid, bool after_tiles) {
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // The tile kernel's share of a plan over `units` (batch rows) x H_kv heads, `tokens` tokens
-// and `keys` keys each: row blocks, and the number of key ranges that takes the least time
-// by a plain model.  A block costs its key tiles and three more for filling and draining, at
-// tile_us each; partials are written and read at 5 TB/s.  rows_bytes: what the rows kernel
-// reads beside it.  Its blocks start on every SM that the tile kernel leaves free, at some
-// 45 GB/s of keys to an SM, and take the others as they become free: so where the tile
-// kernel fits in less than a wave, fewer and longer ranges can be the better choice.
+// and `keys` keys each: row blocks, and the length of a key range, by a plain model.
+//   - A block costs its key tiles and three more for filling and draining, at tile_us each.
+//   - A row block's keys are cut into ranges of `per` tiles and a shorter last one; the full
+//     ranges come first in the grid, so the short ones fill up the SMs that a last wave of
+//     full ones leaves idle (128 row blocks of 128 key tiles on 148 SMs: 113 + 15 tiles
+//     instead of 128).
+//   - Partials are written and read at 5 TB/s.
+//   - rows_bytes: what the rows kernel reads beside it.  Its blocks start on every SM that
+//     the tile kernel leaves free, at some 45 GB/s of keys to an SM, and take the others as
+//     they become free; so where the tile kernel fits in less than a wave, fewer and longer
+//     ranges can be the better choice.
 void plan_tiles(long long units, int H_kv, int group, int tokens, int keys, int D,
                 long long part_bytes, bool joined, double rows_bytes, int& chunk, int& splits,
                 int& blocks, int& ksplit, int& parts) {
@@ -715,33 +721,49 @@ void plan_tiles(long long units, int H_kv, int group, int tokens, int keys, int 
     ksplit = tiles == 1;
     blocks = ksplit ? 1 : ceil_div(tiles, 2);
     const int kt = ceil_div(keys, 128);
-    const double tile_us = (D == 128 ? 2.2 : 1.5) * (ksplit ? 0.6 : 1.0);
+    const long long items = units * H_kv * blocks;
+    // (a row tile's empty warps cost nothing, a half-empty block still its MMAs)
+    const double fill = (double)tokens * group / (256.0 * blocks);
+    const double tile_us = (D == 128 ? 2.2 : 1.8) * (ksplit ? 0.6 : 0.6 + 0.4 * fill);
     const double rows_sm_us = rows_bytes / 45e3;
     double best = 0;
-    splits = 0;
-    for (int s = 1; s <= kt && s <= 512; ++s) {
-        const int per = ceil_div(kt, s);
-        if (s > 1 && ceil_div(kt, per) != s) continue;  // the same ranges as fewer splits
-        const long long n = units * H_kv * blocks * s;
-        const double us = (double)ceil_div(n, kSms) * (per + 3) * tile_us;
-        const double left = rows_sm_us - (n < kSms ? (kSms - n) * us : 0.0);
+    int best_per = 0;
+    auto consider = [&](int per) {
+        const int s = ceil_div(kt, per), rest = kt - (s - 1) * per;
+        const long long longs = items * (rest == per ? s : s - 1), q = longs / kSms,
+                        r = longs % kSms;
+        const long long shorts = rest == per ? 0 : items;
+        const int cl = per + 3, cs = rest + 3;
+        // full ranges wave by wave, then the short ones on the SMs that are free first
+        double end = (double)(q + (r > 0)) * cl;
+        if (shorts > 0) {
+            const long long idle = kSms - r, fit = idle * (r > 0 ? cl / cs : 0);
+            const long long over = shorts - fit;
+            if (over > 0) end += (double)ceil_div(over, kSms) * cs;
+        }
+        const double us = end * tile_us;
+        const double busy = ((double)longs * cl + (double)shorts * cs) * tile_us;
+        const double left = rows_sm_us - (us * kSms - busy);
         const int np = s * (1 + ksplit);
         const double join = np > 1 || joined ? 2.0 * np * part_bytes / 5e6 : 0.0;
         const double all = us + (left > 0 ? left / kSms : 0.0) + join +
                            (np > 1 && !joined ? 3.0 : 0.0);
-        if (splits == 0 || all < best) {
+        if (best_per == 0 || all < best) {
             best = all;
-            splits = s;
+            best_per = per;
         }
-    }
-    chunk = ceil_div(kt, splits) * 128;
+    };
+    const long long most = 4LL * kSms / items > 64 ? 4LL * kSms / items : 64;
+    for (int s = 1; s <= kt && s <= most; ++s) consider(ceil_div(kt, s));
+    const int step = kt / 64 + 1;
+    for (int per = kt - 1; per > kt / 2; per -= step) consider(per);
+    splits = ceil_div(kt, best_per);
+    chunk = best_per * 128;
     parts = splits * (1 + ksplit);
 }
 
-}  // namespace
-
-KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
-               int H_kv, int D, int paged, int page_size) {
+KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
+                 int H_kv, int D, int paged, int page_size) {
     KvPlan p = {};
     const int group = H_q / H_kv;
     const long long rows_o = (long long)max_tokens * group, rows_p = (long long)n_tokens * group;
@@ -793,7 +815,16 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
         p.row_blocks = (int)(blocks < most ? blocks : most);
         long long per = groups / (p.row_blocks * kWarps);  // of a full batch
         if (per < p.min_groups) per = p.min_groups;
-        p.wide_combine = longest / per + p.parts_p > 16;
+        // The combine: a warp to a row (444 blocks of eight resident), or a block to a row
+        // (296 resident) with an eighth of the steps of eight partials, at some 0.8 us a step
+        // beside 2 us a block.  24 x 8 tokens of 16 heads with 16 partials: 3 us or 24 us; 32
+        // rows with 366: 40 us or 5 us.
+        const double steps = (double)(longest / per + 1 + p.parts_p) / 8;
+        const double narrow = ceil_div((long long)B * max_tokens * H_q, 8 * 3 * kSms) *
+                              (2.0 + 0.8 * steps);
+        const double wide = ceil_div((long long)B * max_tokens * H_q, 2 * kSms) *
+                            (2.0 + 0.1 * steps);
+        p.wide_combine = wide < narrow;
         p.j_own = p.kind_p == kKvRows ? H_kv * p.tiles_p : 0;
         const long long js =
             p.j_own + (p.kind_o == kKvRows ? (long long)B * H_kv * p.tiles_o : 0);
@@ -806,6 +837,24 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
     }
     p.workspace = bytes;
     return p;
+}
+
+}  // namespace
+
+// A plan depends on the sizes alone; a call asks for it twice (workspace, launch) and a
+// decode loop asks with the same sizes again, so the thread's last one is kept.
+KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
+               int H_kv, int D, int paged, int page_size) {
+    static thread_local int last[10] = {};
+    static thread_local KvPlan plan;
+    const int key[10] = {B, n_tokens, max_tokens, max_len, prefix_len, H_q, H_kv, D, paged + 1,
+                         page_size};
+    if (std::memcmp(key, last, sizeof key) != 0) {
+        plan = make_plan(B, n_tokens, max_tokens, max_len, prefix_len, H_q, H_kv, D, paged,
+                         page_size);
+        std::memcpy(last, key, sizeof key);
+    }
+    return plan;
 }
 
 cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wait_limit_ns,

@@ -135,6 +135,49 @@ def test_padded_batch_rows_stay(ra_lib):
         ref.check_attention(o[:3], l[:, :3].t(), (want[0], want[1], want[2].t()), "padded")
 
 
+def test_padded_batch_rows_stay_with_many_tokens(ra_lib):
+    """The same where the tensor-core tiles take the rows: a tile that reaches into the next
+    sequence's rows, or into padding full of NaN, keeps to its own."""
+    x = Batch([33, 50], [40, 77], 16, 2, 64, 150, extra_rows=70, seed=3)
+    q = randn(x.N, 4, 64, seed=5)
+    q[83:] = NAN
+    o = torch.full((x.N, 4, 64), 7.0, device=DEV).bfloat16()
+    l = torch.full((4, x.N), 7.0, device=DEV)
+    ra_lib.prefix_attn_fwd(q.to(DEV), *x.gpu("kp", "vp", "cu", "lens", "tables"), 50, max_len=77,
+                           prefix_table=x.ptable.to(DEV), prefix_len=150, out=o, lse=l)
+    assert (o[83:] == 7).all() and (l[:, 83:] == 7).all()
+    want = ref.prefix_attention(q[:83], x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, 150, 0.125)
+    ref.check_attention(o[:83], l[:, :83].t(), (want[0], want[1], want[2].t()), "padded tiles")
+
+
+@pytest.mark.parametrize("Lq", [1, 200])
+def test_cross_key_counts_out_of_bounds(ra_lib, Lq):
+    """A key count past the states is cut to them and reported; a negative one is none."""
+    q, k, v = randn(2, Lq, 2, 64, seed=1), randn(2, 70, 2, 64, seed=2), randn(2, 70, 2, 64, seed=3)
+    o, l = ra_lib.cross_attn_fwd(q.to(DEV), k.to(DEV), v.to(DEV), i32([71, -3]).to(DEV))
+    assert ra_lib.load().ra_sync_status(None) == 5 and ra_lib.load().ra_sync_status(None) == 0
+    want = ref.cross_attention(q, k, v, [70, 0], 0.125)
+    ref.check_attention(o, l.transpose(1, 2), (want[0], want[1], want[2].transpose(1, 2)), "cut")
+
+
+def test_two_calls_at_once(ra_lib):
+    """Calls on two streams at the same time, and the host's next call before the last has
+    run, do not meet in each other's workspace."""
+    x = Batch([1] * 20 + [40], [50 + 9 * i for i in range(20)] + [90], 16, 2, 64, 300, seed=2)
+    args = [(randn(x.N, 4, 64, seed=i).to(DEV), *x.gpu("kp", "vp", "cu", "lens", "tables"), 40)
+            for i in range(2)]
+    kw = dict(max_len=230, prefix_table=x.ptable.to(DEV), prefix_len=300)
+    want = [ra_lib.prefix_attn_fwd(*a, **kw) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = []
+    for _ in range(10):
+        got += [(i, ra_lib.prefix_attn_fwd(*args[i], stream=streams[i], **kw)) for i in range(2)]
+    torch.cuda.synchronize()
+    for i, (o, l) in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
 def test_strided_queries_and_interleaved_pages(ra_lib):
     """q as a slice of a wider projection; K and V pages interleaved in one allocation."""
     x = Batch([3, 1], [50, 20], 16, 2, 64, 40, seed=2)
