@@ -165,55 +165,49 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wid = blockIdx.x * kWarps + warp, n_warps = gridDim.x * kWarps;
 
-    // ---- this warp's stretch of the line: [f0, f0 + cnt)
-    Place x;
+    // ---- this warp's stretch of the line: [f0, f0 + cnt).  Every warp adds up the batch for
+    // itself (entry 0 the prefix, entry e sequence e - 1), then looks for the entry that its
+    // stretch starts in.
     // (the host has checked that the whole line is shorter than 2^31 groups)
-    unsigned per = 0, f0 = 0;
+    Place x;
     int cnt = 0;
-    {
-        auto weight = [&](int b) -> unsigned {
-            if (b >= a.B) return 0;
-            const Seq s = get_seq<R, C::KEYS>(p, b);
-            return (unsigned)(s.groups * s.tiles);
-        };
-        const unsigned w_first = weight(lane);  // of the first 32 sequences: read once
-        const unsigned w_prefix = weight(-1);
-        unsigned mine = w_first;
-        for (int b0 = 32; b0 < a.B; b0 += 32) mine += weight(b0 + lane);
-        const unsigned total = (w_prefix + __reduce_add_sync(0xffffffffu, mine)) * a.H_kv;
-        per = max((total + n_warps - 1) / n_warps, (unsigned)p.p.min_groups);
-        // (a stretch that starts past the end is empty; the product may wrap there)
-        const bool some = wid < (int)((total + per - 1) / per);
-        f0 = per * wid;
-        if (some) {
-            cnt = (int)min(per, total - f0);
-            // the sequence that f0 lies in
-            unsigned at = w_prefix * a.H_kv, rel = f0;
-            int b = -1;
-            if (f0 >= at) {
-                for (int b0 = 0; b0 < a.B; b0 += 32) {
-                    const unsigned w = (b0 == 0 ? w_first : weight(b0 + lane)) * a.H_kv;
-                    unsigned incl = w;
+    auto weight = [&](int e) -> unsigned {
+        if (e > a.B) return 0;
+        const Seq s = get_seq<R, C::KEYS>(p, e - 1);
+        return (unsigned)(s.groups * s.tiles * a.H_kv);
+    };
+    unsigned w = weight(lane), total = w;
+#pragma unroll 4
+    for (int e0 = 32; e0 <= a.B; e0 += 32) total += weight(e0 + lane);
+    total = __reduce_add_sync(0xffffffffu, total);
+    const unsigned per =
+        max((total + n_warps - 1) / n_warps, (unsigned)p.p.min_groups);
+    const unsigned f0 = per * wid;
+    // (a stretch that starts past the end is empty; the product may wrap there)
+    if (wid < (int)((total + per - 1) / per)) {
+        cnt = (int)min(per, total - f0);
+        unsigned at = 0;
+#pragma unroll 1
+        for (int e0 = 0; e0 <= a.B; e0 += 32) {
+            if (e0 > 0) w = weight(e0 + lane);
+            unsigned incl = w;
 #pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const unsigned y = __shfl_up_sync(0xffffffffu, incl, off);
-                        if (lane >= off) incl += y;
-                    }
-                    const unsigned over = __ballot_sync(0xffffffffu, at + incl > f0);
-                    if (over) {
-                        const int l = __ffs(over) - 1;
-                        b = b0 + l;
-                        rel = f0 - at - __shfl_sync(0xffffffffu, incl - w, l);
-                        break;
-                    }
-                    at += __shfl_sync(0xffffffffu, incl, 31);
-                }
+            for (int off = 1; off < 32; off <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
             }
-            x.s = get_seq<R, C::KEYS>(p, b);
-            const unsigned piece = rel / (unsigned)x.s.groups;
-            x.key = (int)(rel - piece * (unsigned)x.s.groups);
-            x.g = (int)(piece / (unsigned)x.s.tiles);
-            x.tile = (int)piece - x.g * x.s.tiles;
+            const unsigned sum = __shfl_sync(0xffffffffu, incl, 31);
+            if (at + sum > f0) {
+                const int l = __ffs(__ballot_sync(0xffffffffu, at + incl > f0)) - 1;
+                const unsigned rel = f0 - at - __shfl_sync(0xffffffffu, incl - w, l);
+                x.s = get_seq<R, C::KEYS>(p, e0 + l - 1);
+                const unsigned piece = rel / (unsigned)x.s.groups;
+                x.key = (int)(rel - piece * (unsigned)x.s.groups);
+                x.g = (int)(piece / (unsigned)x.s.tiles);
+                x.tile = (int)piece - x.g * x.s.tiles;
+                break;
+            }
+            at += sum;
         }
     }
     if (cnt == 0) {
@@ -284,9 +278,6 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
         }
         cp_commit();
     };
-#pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) load(i);
-
     const int r_lo = lane >> 2, c_lo = (lane & 3) * 2;
     const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane's address
     uint32_t qf[MT][D / 16][4];
@@ -295,8 +286,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
     float o[MT][D / 8][4];
     float m[MT][2], l[MT][2], lu[MT][2];
     bool fresh = true;
-    for (int i = 0; i < cnt; ++i) {
-        if (fresh) {  // a new piece: its Q fragments, an empty state
+    for (int i = 1 - C::STAGES; i < cnt; ++i) {
+        // (the first steps, below 0, only fill the ring)
+        if (i >= 0 && fresh) {  // a new piece: its Q fragments, an empty state
             fresh = false;
             const bool causal = a.causal && x.s.b >= 0;
             min_limit = x.s.len;
@@ -338,9 +330,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
                 p.meta[j] = make_int2(wid + j, (int)last - wid + 1);
             }
         }
-        cp_wait<C::STAGES - 2>();
-        __syncwarp();
+        if (i >= 0) {
+            cp_wait<C::STAGES - 2>();
+            __syncwarp();
+        }
         load(i + C::STAGES - 1);
+        if (i < 0) continue;
         const uint32_t kst = ring + (i % C::STAGES) * 2 * C::GROUP_BYTES;
         const uint32_t vst = kst + C::GROUP_BYTES;
         // two accumulation chains (even and odd steps of D) of a 16-key group where registers
