@@ -9,16 +9,18 @@
 // stages that is filled across the borders between heads and sequences, and a softmax state
 // (maximum m, sum l, output O, all fp32) that is written out as a partial result at each
 // border.  No warp waits for another.  A first form with a block per key range and a merge
-// of its four warps' states took 82 us where this takes less (12 sequences of 1001 .. 16384
-// keys, 8 kv heads of 128): its blocks spent some 4 us each on starting, filling and merging.
+// of its four warps' states took 82 us where this takes 73 (12 sequences of 1001 .. 16384
+// keys, 8 kv heads of 128, 427 MB): its blocks spent some 4 us each on starting, filling and
+// merging.
 //
 // Warp w's piece of the j-th (sequence, head, tile) is partial slot w + j (along the line
 // one of the two grows at every border, so no slot is used twice), and the pieces of one j
 // lie next to each other; the warp that has its first key notes where and how many.
 //
 // What bounds it: 16 rows need 4 D flops per key against 4 D bytes of K and V, far below the
-// machine's balance, so it runs at the rate at which K and V arrive.  Hence mma.sync on
-// 16-row fragments (a tcgen05 tile has at least 64 rows) and the deep per-warp rings.
+// machine's balance, so it runs at the rate at which K and V arrive (6.1 TB/s over 786 MB at
+// D = 128, 5.6 at D = 64).  Hence mma.sync on 16-row fragments (a tcgen05 tile has at least
+// 64 rows) and the deep per-warp rings.
 #include <cuda_bf16.h>
 #include <cmath>
 #include <cstring>

@@ -9,6 +9,11 @@
 // and one subtraction): a 32-bit product loses 2^-24 of an angle of up to millions of
 // radians.  The fraction that is left, at most half a turn, is exact enough in 32 bits
 // (relative 2^-24) for sincospif.
+//
+// What bounds it: memory (every vector is read and written once); a small call, the latency of
+// length -> page -> store.  Four tokens to a block, so that a thread has eight 16-byte loads in
+// flight, and they are issued before the places and angles are worked out: 396 MB (16 thousand
+// tokens of 32 + 2 x 8 heads of 128) take 65 us, 6.1 TB/s; loading after them took 72 us.
 #include <cuda_bf16.h>
 #include "kv_internal.h"
 
