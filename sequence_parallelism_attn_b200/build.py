@@ -24,7 +24,7 @@ BINDING = "binding.cpp"
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "attn_sm100.cu", "attn_bwd_sm100.cu", "bwd_static.cu", "attn_fp32.cu", "lse_merge.cu", "permute.cu",
            "api_kv.cu", "paged_append.cu", "kv_rows.cu", "cross_bwd.cu",
-           "kv_tiles_sm100.cu"]
+           "kv_tiles_sm100.cu", "kv_cluster.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
               "-fvisibility=hidden", f"-I{INCLUDE}", f"-I{CSRC}"]

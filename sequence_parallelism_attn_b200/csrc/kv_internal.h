@@ -50,10 +50,10 @@ struct KvArgs {
 };
 
 // How a call is split.  The prefix and the sequences' own keys are each taken by one of two
-// kernels: the tile kernel in ranges of `chunk` keys, each a partial result of its rows (two
+// kernels, or both by a third (kKvCluster): the tile kernel in ranges of `chunk` keys, each a partial result of its rows (two
 // where its warpgroups share a row tile), or the rows kernel, whose warps share the keys out
 // evenly among themselves.  The combine kernel joins the partials.
-constexpr int kKvNone = 0, kKvRows = 1, kKvTiles = 2;
+constexpr int kKvNone = 0, kKvRows = 1, kKvTiles = 2, kKvCluster = 3;
 struct KvPlan {
     int kind_p, chunk_p, splits_p, tiles_p, ksplit_p, parts_p;  // the prefix
     int kind_o, chunk_o, splits_o, tiles_o, ksplit_o, parts_o;  // own keys
@@ -61,6 +61,7 @@ struct KvPlan {
     int row_blocks, j_own;        // its grid; index of the first (sequence, head, tile)
     int min_groups, wide_combine; // fewest key groups of a warp; eight warps join a row
     long long slots;              // its partial slots
+    int cluster;                  // kKvCluster (own keys and prefix together): its blocks
     int direct;                   // a single part: results written without partials
     long long blocks, workspace;  // largest index of a launch (to be below 2^31), bytes
 };
@@ -73,6 +74,7 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& p, unsigned long long wait_
 cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& p, unsigned long long wait_limit_ns,
                             const char** why);
 cudaError_t read_and_clear_kv_tile_error(unsigned int* value);
+cudaError_t read_and_clear_kv_cluster_error(unsigned int* value);
 
 struct CrossBwdArgs {
     const void *q, *k, *v, *out, *dout;

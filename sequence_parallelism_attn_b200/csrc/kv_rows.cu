@@ -21,95 +21,15 @@
 // machine's balance, so it runs at the rate at which K and V arrive (6.1 TB/s over 786 MB at
 // D = 128, 5.6 at D = 64).  Hence mma.sync on 16-row fragments (a tcgen05 tile has at least
 // 64 rows) and the deep per-warp rings.
-#include <cuda_bf16.h>
 #include <cmath>
 #include <cstring>
-#include "kv_internal.h"
-#include "sm100_ptx.cuh"
+#include "kv_rows.cuh"
 
 namespace ra {
 
 __device__ unsigned int g_kv_error_word = 0;
 
 namespace {
-
-constexpr int kWarps = 4;
-// Keys of a group: 8 KB of K and V either way.  At D = 64 a group of 16 spent as much on the
-// softmax's latencies as on its bytes (5.5 TB/s in the long run, against 6.2 at D = 128).
-constexpr int group_keys(int D) { return D == 64 ? 32 : 16; }
-constexpr float kRescale = 8.0f;  // log2 units: the maximum may lag by 2^8
-
-struct RowsParams {
-    KvArgs a;
-    KvPlan p;
-    int group;
-    FastDiv dgroup, dpage, dheads, dtokens;  // by group, page_size, H_q, max_tokens
-    float scale_log2;
-    float* part_o;    // the tile kernel's partials: [part][token][head][D]
-    float* part_lse;  // [part][token][head], log2
-    float* slot_o;    // the rows kernel's: [slot][row of the tile][D]
-    float* slot_lse;  // [slot][row of the tile], log2
-    int2* meta;       // per j: first slot, number of slots
-};
-
-__device__ __forceinline__ int fdiv(int n, const FastDiv& f) {
-    return (int)((__umulhi((uint32_t)n, f.mul) + (uint32_t)n) >> f.shift);
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-constexpr int kBlocksPerSm = 2;  // resident, by registers and by the rings' 96 KB
-
-template <int D, int MT>
-struct RCfg {
-    static constexpr int STAGES = 3;
-    static constexpr int KEYS = group_keys(D);
-    static constexpr int GROUP_BYTES = KEYS * D * 2;           // K or V of one group
-    static constexpr int WARP_BYTES = STAGES * 2 * GROUP_BYTES;
-    static constexpr int SMEM = kWarps * WARP_BYTES;
-    static constexpr int ROWS = MT * 16;
-};
-
-// Byte offset of 16-byte chunk c of row r, chunks permuted within a row so that the eight
-// rows of an ldmatrix fall on different banks.
-template <int D>
-__device__ __forceinline__ uint32_t sw(int r, int c) {
-    return (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
-}
-
-// The line of work.  j: index of a (sequence, head, tile); sequence -1 is the prefix.
-struct Seq {
-    int b, tok0, n_tok, len, groups, tiles;  // groups: key groups of one head and tile
-    const int* table;
-};
 
 template <int R, int KEYS>
 __device__ __forceinline__ Seq get_seq(const RowsParams& p, int b) {
@@ -161,7 +81,7 @@ __device__ __forceinline__ void next_piece(const RowsParams& p, Place& x) {
 template <int D, int MT, bool PAGE16>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(const __grid_constant__ RowsParams p) {
     using C = RCfg<D, MT>;
-    constexpr int R = C::ROWS, kKeys = C::KEYS, NT = kKeys / 8, H16 = kKeys / 16;
+    constexpr int R = C::ROWS, kKeys = C::KEYS, H16 = kKeys / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     const KvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -280,51 +200,13 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
         }
         cp_commit();
     };
-    const int r_lo = lane >> 2, c_lo = (lane & 3) * 2;
-    const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane's address
-    uint32_t qf[MT][D / 16][4];
-    int limit[MT][2];  // keys below it are seen
-    int min_limit = 0;
-    float o[MT][D / 8][4];
-    float m[MT][2], l[MT][2], lu[MT][2];
+    RowState<D, MT> r;
     bool fresh = true;
     for (int i = 1 - C::STAGES; i < cnt; ++i) {
         // (the first steps, below 0, only fill the ring)
         if (i >= 0 && fresh) {  // a new piece: its Q fragments, an empty state
             fresh = false;
-            const bool causal = a.causal && x.s.b >= 0;
-            min_limit = x.s.len;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int row = x.tile * R + mt * 16 + r_lo + 8 * hf;
-                    const bool ok = row < x.s.n_tok * p.group;
-                    const int t = ok ? fdiv(row, p.dgroup) : 0;
-                    const int head = x.g * p.group + (ok ? row - t * p.group : 0);
-                    limit[mt][hf] = ok && causal ? min(x.s.len, x.s.len - x.s.n_tok + t + 1)
-                                                 : x.s.len;
-                    min_limit = min(min_limit, limit[mt][hf]);
-                    const long long off =
-                        (a.cu ? (long long)(x.s.tok0 + t) * a.q_tstride
-                              : (long long)x.s.b * a.q_bstride + (long long)t * a.q_tstride) +
-                        (long long)head * D;
-                    const uint32_t* q32 =
-                        reinterpret_cast<const uint32_t*>((const uint16_t*)a.q + off);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        qf[mt][kk][hf] = ok ? q32[(kk * 16 + c_lo) / 2] : 0u;
-                        qf[mt][kk][2 + hf] = ok ? q32[(kk * 16 + c_lo + 8) / 2] : 0u;
-                    }
-                    m[mt][hf] = -INFINITY;
-                    l[mt][hf] = lu[mt][hf] = 0.f;
-                }
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-            }
-            min_limit = __reduce_min_sync(0xffffffffu, min_limit);
+            r.start(p, x.s, x.g, x.tile, a.causal && x.s.b >= 0);
             if (x.key == 0 && lane == 0) {  // the piece that starts this j: note its slots
                 const unsigned last = (f0 + i + x.s.groups - 1) / per;
                 const int j = x.s.b < 0 ? x.g * p.p.tiles_p + x.tile
@@ -340,106 +222,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
         if (i < 0) continue;
         const uint32_t kst = ring + (i % C::STAGES) * 2 * C::GROUP_BYTES;
         const uint32_t vst = kst + C::GROUP_BYTES;
-        // two accumulation chains (even and odd steps of D) of a 16-key group where registers
-        // allow: with two warps to a scheduler the products' latency shows
-        constexpr int CHAINS = D == 128 && MT == 1 ? 2 : 1;
-        float s[MT][NT][4], s_odd[MT][NT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[mt][n][e] = s_odd[mt][n][e] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int h = 0; h < H16; ++h) {
-                uint32_t kf[4];
-                ldsm4(kf, kst + sw<D>(16 * h + (mi >> 1) * 8 + mr, kk * 2 + (mi & 1)));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float(&acc)[NT][4] = CHAINS == 2 && (kk & 1) ? s_odd[mt] : s[mt];
-                    mma16816(acc[2 * h], qf[mt][kk], kf[0], kf[1]);
-                    mma16816(acc[2 * h + 1], qf[mt][kk], kf[2], kf[3]);
-                }
-            }
-        if (CHAINS == 2)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][n][e] += s_odd[mt][n][e];
-        const int key0 = x.key * kKeys;
-        if (key0 + kKeys > min_limit) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key0 + n * 8 + c_lo + (e & 1) >= limit[mt][e >> 1])
-                            s[mt][n][e] = -INFINITY;
-        }
-        uint32_t pf[MT][H16][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            float alpha[2];
-            bool grew = false;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float mx = fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]);
-#pragma unroll
-                for (int n = 1; n < NT; ++n) mx = fmax3(mx, s[mt][n][2 * hf], s[mt][n][2 * hf + 1]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m_new = mx * p.scale_log2;
-                alpha[hf] = 1.f;
-                // the maximum is moved only when it grew by more than 2^8 (the sums use the
-                // same stale maximum, so the result is the same)
-                if (m_new - m[mt][hf] > kRescale) {
-                    alpha[hf] = ex2_approx(m[mt][hf] - m_new);
-                    m[mt][hf] = m_new;
-                    grew = true;
-                }
-                const float neg = m[mt][hf] == -INFINITY ? 0.f : -m[mt][hf];
-                float sum = 0.f, used = 0.f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float p0 = ex2_approx(fmaf(s[mt][n][2 * hf], p.scale_log2, neg));
-                    const float p1 = ex2_approx(fmaf(s[mt][n][2 * hf + 1], p.scale_log2, neg));
-                    // weights are rounded to bf16 for the tensor cores; l_used sums them as
-                    // they are used, so that the weights applied to V add up to one
-                    const uint32_t pp = pack_bf16x2(p0, p1);
-                    pf[mt][n >> 1][2 * (n & 1) + hf] = pp;
-                    sum += p0 + p1;
-                    used += __uint_as_float(pp << 16) + __uint_as_float(pp & 0xffff0000u);
-                }
-                l[mt][hf] = l[mt][hf] * alpha[hf] + sum;
-                lu[mt][hf] = lu[mt][hf] * alpha[hf] + used;
-            }
-            if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[mt][n][0] *= alpha[0];
-                    o[mt][n][1] *= alpha[0];
-                    o[mt][n][2] *= alpha[1];
-                    o[mt][n][3] *= alpha[1];
-                }
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < H16; ++h)
-#pragma unroll
-            for (int nn = 0; nn < D / 16; ++nn) {
-                uint32_t vf[4];
-                ldsm4_t(vf, vst + sw<D>(16 * h + (mi & 1) * 8 + mr, nn * 2 + (mi >> 1)));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma16816(o[mt][2 * nn], pf[mt][h], vf[0], vf[1]);
-                    mma16816(o[mt][2 * nn + 1], pf[mt][h], vf[2], vf[3]);
-                }
-            }
+        r.attend(p, kst, vst, x.key * kKeys);
         // ---- the piece's end: its partial result
         const bool border = x.key + 1 == x.s.groups;
         if (border || i + 1 == cnt) {
@@ -452,24 +235,24 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
                     for (int off = 1; off <= 2; off <<= 1) {
-                        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], off);
-                        lu[mt][hf] += __shfl_xor_sync(0xffffffffu, lu[mt][hf], off);
+                        r.l[mt][hf] += __shfl_xor_sync(0xffffffffu, r.l[mt][hf], off);
+                        r.lu[mt][hf] += __shfl_xor_sync(0xffffffffu, r.lu[mt][hf], off);
                     }
-                    const int r = mt * 16 + r_lo + 8 * hf;
-                    if (x.tile * R + r < x.s.n_tok * p.group) {
+                    const int row = mt * 16 + (lane >> 2) + 8 * hf;
+                    if (x.tile * R + row < x.s.n_tok * p.group) {
                         // no key seen: every m is -inf and every sum 0 (a NaN score leaves m
                         // as it was but makes the sums NaN, which must come through)
-                        const float inv = lu[mt][hf] == 0.f ? 0.f : 1.f / lu[mt][hf];
-                        float* dst = p.slot_o + (slot + r) * D + c_lo;
+                        const float lr = r.l[mt][hf], mr = r.m[mt][hf];
+                        const float inv = r.lu[mt][hf] == 0.f ? 0.f : 1.f / r.lu[mt][hf];
+                        float* dst = p.slot_o + (slot + row) * D + (lane & 3) * 2;
 #pragma unroll
                         for (int n = 0; n < D / 8; ++n)
                             *reinterpret_cast<float2*>(dst + n * 8) =
-                                make_float2(o[mt][n][2 * hf] * inv, o[mt][n][2 * hf + 1] * inv);
+                                make_float2(r.o[mt][n][2 * hf] * inv, r.o[mt][n][2 * hf + 1] * inv);
                         if ((lane & 3) == 0)
-                            p.slot_lse[slot + r] =
-                                l[mt][hf] == 0.f
-                                    ? -INFINITY
-                                    : (m[mt][hf] == -INFINITY ? 0.f : m[mt][hf]) + log2f(l[mt][hf]);
+                            p.slot_lse[slot + row] =
+                                lr == 0.f ? -INFINITY
+                                          : (mr == -INFINITY ? 0.f : mr) + log2f(lr);
                     }
                 }
             fresh = true;
@@ -759,11 +542,46 @@ void plan_tiles(long long units, int H_kv, int group, int tokens, int keys, int 
     parts = splits * (1 + ksplit);
 }
 
+// Whether clusters of blocks take the call: every (sequence, kv head) one, as many blocks to
+// each as run beside one another (two an SM, up to the portable eight; a cluster's blocks share
+// one of the GPCs of some 18 SMs, so 28 clusters of eight fit, not 37).  Measured, us, for J
+// (sequence, head) pairs of D = 128 with equal lengths, clusters against rows + combine:
+//   J = 2:  2048 keys 7.0, 8.9    8192 keys 14.4, 11.7
+//   J = 64: 512 keys 7.2, 9.3     2048 keys 15.8, 17.7     8192 keys 44, 50
+// which is about 4.5 + the larger of 0.62 a group of a warp and the keys at 6.2 TB/s, against
+// 8.5 + the keys at 6 TB/s.  The cluster's time is that of the longest sequence, the rows
+// kernel's that of the whole batch (whose lengths are not known here: 0.75 of their bound), and
+// only the clusters read the prefix anew for every sequence.
+bool plan_cluster(int B, long long rows, long long rows_p, int max_len, int prefix_len, int H_kv,
+                  int D, KvPlan& p) {
+    const long long js = (long long)B * H_kv;
+    int c = 8;
+    while (c > 1 && js * c > (c == 8 ? 224 : c == 4 ? 272 : kBlocksPerSm * kSms)) c /= 2;
+    if (js * c > kBlocksPerSm * kSms) return false;
+    const long long go = ceil_div(max_len, group_keys(D)), gp = ceil_div(prefix_len, group_keys(D));
+    const double mb = 8192e-6;  // of a group
+    const double steps = 0.62 * ceil_div(go + gp, kWarps * c), read = js * (go + gp) * mb / 6.2;
+    const double cluster = 4.5 + (steps > read ? steps : read);
+    const double other = 8.5 + 0.75 * js * go * mb / 6.0 + H_kv * gp * mb / 6.0 +
+                         (rows_p > 32 && prefix_len > 0 ? 4.0 : 0.0);  // the tile kernel beside
+    if (cluster > other) return false;
+    p = KvPlan{};
+    p.kind_o = kKvCluster;
+    p.mt = rows > 16 ? 2 : 1;
+    p.tiles_o = 1;
+    p.cluster = c;
+    p.direct = 1;
+    p.blocks = js * c;
+    return true;
+}
+
 KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_len, int H_q,
                  int H_kv, int D, int paged, int page_size) {
     KvPlan p = {};
     const int group = H_q / H_kv;
     const long long rows_o = (long long)max_tokens * group, rows_p = (long long)n_tokens * group;
+    if (rows_o <= 32 && plan_cluster(B, rows_o, rows_p, max_len, prefix_len, H_kv, D, p))
+        return p;
     // the tile kernel takes whole groups of heads, and pages that divide its 128-key tiles
     const bool tiles_ok =
         group <= 128 && (!paged || (page_size >= 8 && (page_size & (page_size - 1)) == 0));
@@ -871,6 +689,10 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
     p.dheads = make_fastdiv((uint32_t)a.H_q);
     p.dtokens = make_fastdiv((uint32_t)a.max_tokens);
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+    if (plan.kind_o == kKvCluster) {
+        *why = "cluster attention launch";
+        return launch_kv_cluster(p);
+    }
     const long long rows = (long long)a.n_tokens * a.H_q;
     p.part_o = (float*)a.workspace;
     p.part_lse = p.part_o + (long long)(plan.parts_p + plan.parts_o) * rows * a.D;

@@ -89,6 +89,14 @@ PREFIX = [  # n, lens, page, hq, hkv, d, prefix
      4, 2, 64, 19),
     ([1] * 100, [1 + 37 * i % 90 for i in range(100)], 16, 2, 2, 128, 0),
     ([0] * 40 + [1], [0] * 40 + [33], 16, 2, 1, 64, 0),
+    # clusters of eight, four and two blocks to a (sequence, head), and a block to each; page
+    # borders, prefix borders and row fragments inside a warp's groups
+    ([1, 1], [700, 1], 16, 16, 8, 64, 333),
+    ([3, 2, 1], [300, 40, 7], 16, 16, 2, 128, 1001),
+    ([1] * 5, [17, 400, 33, 90, 1], 16, 64, 8, 128, 17),
+    ([1] * 40, [1 + 29 * i % 200 for i in range(40)], 16, 8, 4, 64, 40),
+    ([2] * 37, [2 + 31 * i % 150 for i in range(37)], 16, 8, 8, 64, 0),
+    ([2, 0, 1], [50, 0, 90], 3, 4, 2, 128, 100),
 ]
 
 

@@ -55,7 +55,8 @@ def test_append_refusals(lib, kw, status):
     (dict(max_len=0), 1), (dict(max_len=65), 1), (dict(hq=5), 1), (dict(d=32), 2),
     (dict(page=0), 1), (dict(ps=100), 1), (dict(scale=0.0), 1), (dict(scale=float("inf")), 1),
     (dict(scale=float("nan")), 1), (dict(dt=1), 2), (dict(odt=3), 1), (dict(out=0), 1),
-    (dict(lse=FAKE + 4), 1), (dict(ws=0), 1), (dict(ws=FAKE + 8), 1), (dict(wsb=16), 1),
+    (dict(lse=FAKE + 4), 1), (dict(ws=0, plen=1 << 17), 1), (dict(ws=FAKE + 8, plen=1 << 17), 1),
+    (dict(wsb=16, plen=1 << 17), 1),
 ])
 def test_prefix_refusals(lib, kw, status):
     assert call(lib, "ra_prefix_attn_fwd", PREFIX, kw) == status
@@ -76,14 +77,17 @@ def test_cross_refusals(lib, kw, status):
 
 def test_workspace_sizes(lib):
     lib.ra_prefix_attn_workspace.restype = I64
-    small = lib.ra_prefix_attn_workspace(4, 4, 1, 100, 0, 8, 2, 64, 16)
-    assert 0 < small < lib.ra_prefix_attn_workspace(4, 4, 1, 100, 1000, 8, 2, 64, 16)
+    # few rows over a moderate number of keys: one kernel, no partial results
+    assert lib.ra_prefix_attn_workspace(4, 4, 1, 100, 0, 8, 2, 64, 16) == 0
+    some = lib.ra_prefix_attn_workspace(4, 4, 1, 1 << 17, 0, 8, 2, 64, 16)
+    assert 0 < some < lib.ra_prefix_attn_workspace(4, 4, 1, 1 << 17, 1000, 8, 2, 64, 16)
     assert lib.ra_prefix_attn_workspace(0, 4, 1, 100, 0, 8, 2, 64, 16) == 0
     # bounded by the resident warps, not by the keys
     assert lib.ra_prefix_attn_workspace(1, 1, 1, 1 << 24, 1 << 24, 32, 8, 128, 16) < 32 << 20
     # many rows in one range of keys: results are written without partials
     assert lib.ra_cross_attn_workspace(64, 300, 100, 8, 8, 64) == 0
     assert lib.ra_cross_attn_workspace(1, 30, 1000, 8, 2, 64) > 0
+    assert lib.ra_cross_attn_workspace(1, 1, 1000, 8, 2, 64) == 0
 
 
 def test_binding_refusals():
