@@ -59,6 +59,7 @@ struct KvPlan {
     int kind_o, chunk_o, splits_o, tiles_o, ksplit_o, parts_o;  // own keys
     int mt;                       // rows kernel: 16-row fragments of a row tile
     int row_blocks, j_own;        // its grid; index of the first (sequence, head, tile)
+    int heads_log;                // log2 of the kv heads that its warps take side by side
     int min_groups, wide_combine; // fewest key groups of a warp; eight warps join a row
     long long slots;              // its partial slots
     int cluster;                  // kKvCluster (own keys and prefix together): its blocks

@@ -1,26 +1,29 @@
 // kv_rows.cu -- attention of few query rows over many keys: the single-token form of the
 // paged, prefix and cross attention, and the joining of every form's partial results.
 //
-// Work is counted in groups of 16 keys (32 at D = 64) of (sequence, kv head, row tile) -- row tiles of 16 or 32
-// rows, tokens x the query heads that share the kv head -- laid end to end: the prefix first
-// (rows of the whole batch, so its keys are read once), then every sequence's own keys.  The
-// resident warps (four to a block, two blocks to an SM) each take an equal stretch of that
-// line, whatever the sequences' lengths, and run it as one stream: a ring of cp.async
-// stages that is filled across the borders between heads and sequences, and a softmax state
-// (maximum m, sum l, output O, all fp32) that is written out as a partial result at each
-// border.  No warp waits for another.  A first form with a block per key range and a merge
-// of its four warps' states took 82 us where this takes 73 (12 sequences of 1001 .. 16384
-// keys, 8 kv heads of 128, 427 MB): its blocks spent some 4 us each on starting, filling and
-// merging.
+// Work is counted in groups of 16 keys (32 at D = 64) of (sequence, kv head, row tile) -- row
+// tiles of 16 or 32 rows, tokens x the query heads that share the kv head -- laid end to end:
+// the prefix first (rows of the whole batch, so its keys are read once), then every
+// sequence's own keys.  The resident warps (four to a block, two blocks to an SM) each take an
+// equal stretch of that line, whatever the sequences' lengths, and run it as one stream: a
+// ring of cp.async stages that is filled across the borders between heads and sequences, and
+// a softmax state (maximum m, sum l, output O, all fp32) that is written out as a partial
+// result at each border.  No warp waits for another.  A first form with a block per key range
+// and a merge of its four warps' states took 82 us where this takes 74 (12 sequences of 1001
+// .. 16384 keys, 8 kv heads of 128, 427 MB): its blocks spent some 4 us each on starting,
+// filling and merging.
 //
-// Warp w's piece of the j-th (sequence, head, tile) is partial slot w + j (along the line
-// one of the two grows at every border, so no slot is used twice), and the pieces of one j
-// lie next to each other; the warp that has its first key notes where and how many.
+// Up to four neighbouring kv heads are walked side by side by as many warps (each head's row
+// of a token is 128 or 256 bytes; apart, 16 heads of 64 were read at 5.4 TB/s over 786 MB,
+// side by side at 6.2).  Walker w's piece of the j-th (sequence, heads, tile) is partial slot
+// w + j of each head (along the line one of the two grows at every border, so no slot is used
+// twice), and the pieces of one j lie next to each other; the warp that has its first key
+// notes where and how many.
 //
 // What bounds it: 16 rows need 4 D flops per key against 4 D bytes of K and V, far below the
-// machine's balance, so it runs at the rate at which K and V arrive (6.1 TB/s over 786 MB at
-// D = 128, 5.6 at D = 64).  Hence mma.sync on 16-row fragments (a tcgen05 tile has at least
-// 64 rows) and the deep per-warp rings.
+// machine's balance, so it runs at the rate at which K and V arrive (6.2 TB/s over 786 MB).
+// Hence mma.sync on 16-row fragments (a tcgen05 tile has at least 64 rows) and the deep
+// per-warp rings.
 #include <cmath>
 #include <cstring>
 #include "kv_rows.cuh"
@@ -69,7 +72,7 @@ __device__ __forceinline__ void next_piece(const RowsParams& p, Place& x) {
     x.key = 0;
     if (++x.tile < x.s.tiles) return;
     x.tile = 0;
-    if (++x.g < p.a.H_kv) return;
+    if (++x.g < (p.a.H_kv >> p.p.heads_log)) return;
     x.g = 0;
     do {
         x.s = get_seq<R, KEYS>(p, x.s.b + 1);
@@ -85,7 +88,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
     extern __shared__ __align__(128) uint8_t smem[];
     const KvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int wid = blockIdx.x * kWarps + warp, n_warps = gridDim.x * kWarps;
+    // 2^hl neighbouring warps walk the line together, each for one of as many neighbouring
+    // kv heads: a token's heads lie side by side in memory and are then read side by side
+    const int hl = p.p.heads_log, hs = warp & ((1 << hl) - 1);
+    const int wid = (int)(blockIdx.x * kWarps + warp) >> hl;
+    const int n_warps = (int)(gridDim.x * kWarps) >> hl;
 
     // ---- this warp's stretch of the line: [f0, f0 + cnt).  Every warp adds up the batch for
     // itself (entry 0 the prefix, entry e sequence e - 1), then looks for the entry that its
@@ -96,7 +103,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
     auto weight = [&](int e) -> unsigned {
         if (e > a.B) return 0;
         const Seq s = get_seq<R, C::KEYS>(p, e - 1);
-        return (unsigned)(s.groups * s.tiles * a.H_kv);
+        return (unsigned)(s.groups * s.tiles * (a.H_kv >> hl));
     };
     unsigned w = weight(lane), total = w;
 #pragma unroll 4
@@ -187,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
                         off = (long long)look_up(y.s.table, key) * a.page_stride +
                               (long long)(key - fdiv(key, p.dpage) * a.page_size) * a.kv_tstride;
                     }
-                    off += (long long)y.g * D + c * 8;
+                    off += (long long)((y.g << hl) + hs) * D + c * 8;
                     const uint32_t dst = st + sw<D>(16 * h + r, c);
                     cp_async16(dst, (const uint16_t*)a.k + off, ok);
                     cp_async16(dst + C::GROUP_BYTES, (const uint16_t*)a.v + off, ok);
@@ -202,16 +209,24 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
     };
     RowState<D, MT> r;
     bool fresh = true;
+    // the slot of the piece that x is in: a share of the slots to each of the warp group's heads
+    auto slot_of = [&]() {
+        const int jq = x.s.b < 0 ? x.g * p.p.tiles_p + x.tile
+                                 : (p.p.j_own >> hl) +
+                                       (x.s.b * (a.H_kv >> hl) + x.g) * p.p.tiles_o + x.tile;
+        return hs * ((int)p.p.slots >> hl) + wid + jq;
+    };
     for (int i = 1 - C::STAGES; i < cnt; ++i) {
         // (the first steps, below 0, only fill the ring)
         if (i >= 0 && fresh) {  // a new piece: its Q fragments, an empty state
             fresh = false;
-            r.start(p, x.s, x.g, x.tile, a.causal && x.s.b >= 0);
+            r.start(p, x.s, (x.g << hl) + hs, x.tile, a.causal && x.s.b >= 0);
             if (x.key == 0 && lane == 0) {  // the piece that starts this j: note its slots
                 const unsigned last = (f0 + i + x.s.groups - 1) / per;
-                const int j = x.s.b < 0 ? x.g * p.p.tiles_p + x.tile
-                                        : p.p.j_own + (x.s.b * a.H_kv + x.g) * p.p.tiles_o + x.tile;
-                p.meta[j] = make_int2(wid + j, (int)last - wid + 1);
+                const int g = (x.g << hl) + hs;
+                const int j = x.s.b < 0 ? g * p.p.tiles_p + x.tile
+                                        : p.p.j_own + (x.s.b * a.H_kv + g) * p.p.tiles_o + x.tile;
+                p.meta[j] = make_int2(slot_of(), (int)last - wid + 1);
             }
         }
         if (i >= 0) {
@@ -226,9 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
         // ---- the piece's end: its partial result
         const bool border = x.key + 1 == x.s.groups;
         if (border || i + 1 == cnt) {
-            const int j = x.s.b < 0 ? x.g * p.p.tiles_p + x.tile
-                                    : p.p.j_own + (x.s.b * a.H_kv + x.g) * p.p.tiles_o + x.tile;
-            const long long slot = (long long)(wid + j) * R;
+            const long long slot = (long long)slot_of() * R;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -640,6 +653,7 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
         const double wide = ceil_div((long long)B * max_tokens * H_q, 2 * kSms) *
                             (2.0 + 0.1 * steps);
         p.wide_combine = wide < narrow;
+        p.heads_log = H_kv % 4 == 0 ? 2 : H_kv % 2 == 0 ? 1 : 0;
         p.j_own = p.kind_p == kKvRows ? H_kv * p.tiles_p : 0;
         const long long js =
             p.j_own + (p.kind_o == kKvRows ? (long long)B * H_kv * p.tiles_o : 0);

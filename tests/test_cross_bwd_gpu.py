@@ -144,3 +144,34 @@ def test_fp32_inputs_are_refused(ra_lib):
         autograd.cross_attention(x, x, x)
     with pytest.raises(ValueError):
         ra_lib.cross_attn_bwd(x.bfloat16(), x.bfloat16(), x.bfloat16(), x, x[..., 0], x)
+
+
+def test_captured_training_step(ra_lib):
+    """A training step through autograd, captured: the gradients of every replay are those of
+    the inputs that it finds."""
+    from sequence_parallelism_attn_b200 import autograd
+    q, kv, do, lens = inputs(7, 21)
+    kv = kv.nan_to_num(0)
+    ql, kl, vl = (x.to(DEV).contiguous().requires_grad_()
+                  for x in (q, kv[:, :, 0], kv[:, :, 1]))
+    dd, ln = do.to(DEV), i32(lens).to(DEV)
+
+    def step():
+        return torch.autograd.grad(autograd.cross_attention(ql, kl, vl, ln), (ql, kl, vl), dd)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = step()
+    for seed in (22, 23):
+        q = randn(*q.shape, seed=seed)
+        with torch.no_grad():
+            ql.copy_(q)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.cross_backward(q, kv[:, :, 0], kv[:, :, 1], lens, do, q.shape[-1] ** -0.5)
+        ref.check_grads(g, want, str(seed))

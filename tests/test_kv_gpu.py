@@ -97,6 +97,7 @@ PREFIX = [  # n, lens, page, hq, hkv, d, prefix
     ([1] * 40, [1 + 29 * i % 200 for i in range(40)], 16, 8, 4, 64, 40),
     ([2] * 37, [2 + 31 * i % 150 for i in range(37)], 16, 8, 8, 64, 0),
     ([2, 0, 1], [50, 0, 90], 3, 4, 2, 128, 100),
+    ([1] * 2500, [1 + 5 * i % 23 for i in range(2500)], 16, 1, 1, 64, 5),  # many sequences
 ]
 
 
@@ -112,6 +113,21 @@ def test_prefix_attention(ra_lib, case, out_dtype):
     assert ra_lib.ra_sync_status() == 0
     want = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, plen, d ** -0.5)
     ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), f"case {case}")
+
+
+@pytest.mark.parametrize("n,lens", [([1, 1], [20, 3]), ([1] * 40, [9] * 40), ([70, 2], [75, 9])])
+def test_bounds_far_above_the_lengths(ra_lib, n, lens):
+    """Without max_len the tables' capacity is the bound: far above the lengths here, which
+    are what is read."""
+    x = Batch(n, lens, 64, 2, 64, 70, seed=9)
+    wide = torch.cat([x.tables, torch.full((len(n), 4000), 1 << 29, dtype=torch.int32)], 1)
+    q = randn(x.N, 4, 64, seed=1)
+    kp, vp, cu, lens_, pt = x.gpu("kp", "vp", "cu", "lens", "ptable")
+    o, l = ra_lib.prefix_attn_fwd(q.to(DEV), kp, vp, cu, lens_, wide.to(DEV), max(n) + 100,
+                                  prefix_table=pt, prefix_len=70)
+    assert ra_lib.ra_sync_status() == 0
+    want = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, 70, 0.125)
+    ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), "wide")
 
 
 def test_rows_that_see_nothing(ra_lib):
