@@ -81,7 +81,7 @@ struct __align__(64) BwdParams {
 // arithmetic per tile).  Cross attention is the contiguous form without causal order whose
 // L query rows and Lc keys differ in number (P = 1), with a key count per batch row.  Measured
 // (8 batch rows, 9 key tiles): a key tile takes 6.8 us + 2.1 us per query tile at D = 64, 10 us +
-// 3.2 us at D = 128; 2 x 2048 queries of 32 heads over 4096 keys of 8 heads of 128, 845 TFLOP/s.
+// 3.2 us at D = 128; 2 x 2048 queries of 32 heads over 4096 keys of 8 heads of 128, 830 TFLOP/s.
 constexpr int kLayoutContiguous = 0, kLayoutZigzag = 1, kLayoutPacked = 2, kLayoutCross = 3;
 
 // Cross attention: the keys of batch row b.
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const uint16_t* __restri
 }
 
 // The same for cross attention, 16 bytes a lane: D/8 lanes to a row (the form above reads 2
-// bytes a lane and took 12 us where this takes 5: 8 x 447 queries, 16 heads of 64).  The two
+// bytes a lane and took 12 us where this takes 8, cold: 8 x 447 queries, 16 heads of 64).  The two
 // differ in the order of a row's sum, so the ring's forms keep theirs, and their bits.
 template <int D>
 __global__ void __launch_bounds__(256) cross_delta_kernel(const uint4* __restrict__ out,

@@ -21,7 +21,7 @@
 // us at D = 128 and 1.86 us at D = 64, where one row to a thread leaves the softmax's latency
 // in sight (MUFU 34%, issue slots 29% busy); a block costs some 6 us beside its key tiles.
 // Below 128 rows the rate at which K and V arrive.  1000 tokens of 32 heads behind 16384 keys
-// of 8 heads of 128: 284 us, 950 TFLOP/s, at the power cap.
+// of 8 heads of 128: 290 us, 930 TFLOP/s, at the power cap.
 //
 // Every wait is bounded, as in attn_sm100.cu.
 #include <cuda.h>
