@@ -428,7 +428,8 @@ RA_API ra_status ra_ulysses_head2seq_grouped(const void* in, void* out, int P, i
  *   - Batch: B sequences with n_b >= 0 new tokens each, ragged: the tokens of sequence b are
  *     rows cu_tokens[b] .. cu_tokens[b+1]-1 of q, k, v and out (cu_tokens: device int32,
  *     [B+1], not decreasing, starting at >= 0).  Rows at or past cu_tokens[B] (a padded
- *     batch) are neither read nor written.  n_tokens: rows of the token tensors, the host's
+ *     batch) and rows before cu_tokens[0] (a slice of a batch, given with all its token
+ *     rows) take no part: nothing depends on them and they are not written.  n_tokens: rows of the token tensors, the host's
  *     bound on cu_tokens[B]; max_tokens: the host's bound on every n_b.
  *   - seq_lens: device int32, [B]: keys of sequence b's own in the cache, its new tokens
  *     included (they are the last n_b of them).

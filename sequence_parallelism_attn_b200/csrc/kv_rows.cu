@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     const int i_tok = fdiv(idx, p.dheads), head = idx - i_tok * a.H_q;
     int b = 0, t = 0, tok = i_tok;
     bool live;
-    const int end = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;  // rows from here on stay
+    // rows before the first sequence's and from the last one's end on stay as they are
+    const int begin = a.cu ? max(a.cu[0], 0) : 0;
+    const int end = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;
     if (p.p.kind_o == kKvRows) {
         b = fdiv(i_tok, p.dtokens);
         t = i_tok - b * a.max_tokens;
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
             live = t < n && tok < end;
         }
     } else {
-        live = tok < end;
+        live = tok >= begin && tok < end;
     }
     if (!live) {
         pdl_wait();  // the end of this grid has to mean the end of those before it

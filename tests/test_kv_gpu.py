@@ -174,6 +174,39 @@ def test_padded_batch_rows_stay_with_many_tokens(ra_lib):
     ref.check_attention(o[:83], l[:, :83].t(), (want[0], want[1], want[2].t()), "padded tiles")
 
 
+@pytest.mark.parametrize("n,plen", [([3, 1, 2, 1], 0), ([3, 1, 2, 1], 20000), ([40, 30, 50, 33], 0),
+                                    ([40, 30, 50, 33], 150), ([20, 20, 1, 1], 20000)])
+def test_slice_of_a_batch(ra_lib, n, plen):
+    """The last two sequences of a batch, given with all of its token rows: the rows of the
+    others stay as they were, in the append too, whichever kernel takes the rows."""
+    x = Batch(n, [m + 9 * i + 300 for i, m in enumerate(n)], 16, 2, 64, plen, extra_rows=3, seed=8)
+    at, end = int(x.cu[2]), int(x.cu[4])
+    q = randn(x.N, 4, 64, seed=5)
+    q[:at] = q[end:] = NAN
+    o = torch.full((x.N, 4, 64), 7.0, device=DEV)
+    l = torch.full((4, x.N), 7.0, device=DEV)
+    kp, vp, cu, lens, tables, pt = x.gpu("kp", "vp", "cu", "lens", "tables", "ptable")
+    meta = (cu[2:].clone(), lens[2:].clone(), tables[2:].clone())
+    ra_lib.prefix_attn_fwd(q.to(DEV), kp, vp, *meta, max(n[2:]), prefix_table=pt, prefix_len=plen,
+                           out=o, lse=l)
+    assert ra_lib.ra_sync_status() == 0
+    for rows in (slice(0, at), slice(end, None)):
+        assert (o[rows] == 7).all() and (l[:, rows] == 7).all()
+    want = ref.prefix_attention(q[:end], x.kp, x.vp, x.cu[2:], x.lens[2:], x.tables[2:], x.ptable,
+                                plen, 0.125)
+    ref.check_attention(o[at:end], l[:, at:end].t(),
+                        (want[0][at:], want[1][at:], want[2].t()[at:]), "slice")
+    kv = randn(x.N, 2, 64, seed=6).to(DEV)
+    whole = vp.clone()
+    q_out = torch.full_like(q, 7.0).to(DEV)
+    ra_lib.paged_kv_append(q.to(DEV), kv, kv, kp, vp, *meta, None, max(n[2:]), q_out=q_out)
+    assert (q_out[:at] == 7).all() and (q_out[end:] == 7).all()
+    assert torch.equal(q_out[at:end], q[at:end].to(DEV))
+    for b in (0, 1):  # the other sequences' pages are not touched
+        used = tables[b, :-(-int(x.lens[b]) // 16)].long()
+        assert torch.equal(vp[used].nan_to_num(9e9), whole[used].nan_to_num(9e9))
+
+
 @pytest.mark.parametrize("Lq", [1, 200])
 def test_cross_key_counts_out_of_bounds(ra_lib, Lq):
     """A key count past the states is cut to them and reported; a negative one is none."""
