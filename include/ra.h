@@ -438,8 +438,8 @@ RA_API ra_status ra_ulysses_head2seq_grouped(const void* in, void* out, int P, i
  *   - The device arrays may change between launches of a captured graph; host arguments are
  *     bounds and stay.  The first call of a kind in a process loads its kernels: make it
  *     before a capture.
- *   - Device values outside their bounds (n_b > max_tokens, seq_lens[b] > max_len or < n_b
- *     for the append, a page id outside [0, n_pages)) are never followed: the kernel skips
+ *   - Device values outside their bounds (cu_tokens below 0, decreasing or above n_tokens,
+ *     n_b > max_tokens, seq_lens[b] > max_len or < n_b for the append, a page id outside [0, n_pages)) are never followed: the kernel skips
  *     or clamps them, what it writes for that sequence is undefined, and ra_sync_status()
  *     returns RA_ERR_INDEX.
  */

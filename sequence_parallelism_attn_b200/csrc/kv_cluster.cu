@@ -75,12 +75,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     s.b = j / a.H_kv;
     const bool reports = rank == 0 && threadIdx.x == 0 && g == 0 && tile == 0;
     if (a.cu) {
-        s.tok0 = max(a.cu[s.b], 0);
-        s.n_tok = min(a.cu[s.b + 1], a.n_tokens) - s.tok0;
-        if (s.n_tok > a.max_tokens) {
-            if (reports) atomicOr(&g_kv_cluster_error_word, kKvErrTokens);
-            s.n_tok = a.max_tokens;
-        }
+        const TokenRows rows = token_rows(a.cu, s.b, a.n_tokens, a.max_tokens);
+        if (rows.bad && reports) atomicOr(&g_kv_cluster_error_word, kKvErrTokens);
+        s.tok0 = rows.first;
+        s.n_tok = min(rows.n, a.max_tokens);
     } else {
         s.tok0 = s.b * a.max_tokens;
         s.n_tok = a.max_tokens;

@@ -13,6 +13,22 @@ constexpr int kSms = 148;  // a B200's SMs: the work split is planned for them, 
 // Bits of the device's cache error word (read and cleared by ra_sync_status).
 constexpr unsigned kKvErrTokens = 1u, kKvErrLength = 2u, kKvErrPage = 4u;
 
+// Sequence b's token rows: the first, and their number, kept within the token tensors
+// whatever cu holds; bad where it was outside the call's bounds.
+struct TokenRows {
+    int first, n;
+    bool bad;
+};
+__device__ __forceinline__ TokenRows token_rows(const int* cu, int b, int n_tokens,
+                                                int max_tokens) {
+    const int c0 = cu[b], c1 = cu[b + 1];
+    TokenRows r;
+    r.first = min(max(c0, 0), n_tokens);
+    r.n = max(min(c1, n_tokens), r.first) - r.first;
+    r.bad = c0 < 0 || c1 < c0 || c1 > n_tokens || c1 - c0 > max_tokens;
+    return r;
+}
+
 struct AppendArgs {
     const void *q, *k, *v;
     long long q_tstride, k_tstride, v_tstride, q_out_tstride;  // elements between tokens

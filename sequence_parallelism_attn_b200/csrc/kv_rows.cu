@@ -46,8 +46,9 @@ __device__ __forceinline__ Seq get_seq(const RowsParams& p, int b) {
         s.table = a.prefix_table;
     } else {
         if (a.cu) {
-            s.tok0 = max(a.cu[b], 0);
-            s.n_tok = min(min(a.cu[b + 1], a.n_tokens) - s.tok0, a.max_tokens);
+            const TokenRows rows = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
+            s.tok0 = rows.first;
+            s.n_tok = min(rows.n, a.max_tokens);
         } else {
             s.tok0 = b * a.max_tokens;
             s.n_tok = a.max_tokens;
@@ -306,11 +307,11 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         t = i_tok - b * a.max_tokens;
         live = b < a.B;
         if (live && a.cu) {
-            const int c0 = max(a.cu[b], 0), n = min(a.cu[b + 1], a.n_tokens) - c0;
-            if (n > a.max_tokens && t == 0 && head == 0 && lane == 0)
+            const TokenRows rows_b = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
+            if (rows_b.bad && t == 0 && head == 0 && lane == 0)
                 atomicOr(&g_kv_error_word, kKvErrTokens);
-            tok = c0 + t;
-            live = t < n && tok < end;
+            tok = rows_b.first + t;
+            live = t < rows_b.n && tok < end;
         }
     } else {
         live = tok >= begin && tok < end;

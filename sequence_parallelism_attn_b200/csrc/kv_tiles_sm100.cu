@@ -198,10 +198,10 @@ __device__ __forceinline__ bool make_item(const TileParams& p, Item& x) {
         x.b = item / p.splits_o;
         const bool first = threadIdx.x == 0 && split == 0;
         if (a.cu) {
-            x.tok0 = max(a.cu[x.b], 0);
-            x.n_tok = min(a.cu[x.b + 1], a.n_tokens) - x.tok0;
-            if (x.n_tok > a.max_tokens && first)
-                atomicOr(&g_kv_tile_error_word, kKvErrTokens << 8);
+            const TokenRows rows = token_rows(a.cu, x.b, a.n_tokens, a.max_tokens);
+            if (first && rows.bad) atomicOr(&g_kv_tile_error_word, kKvErrTokens << 8);
+            x.tok0 = rows.first;
+            x.n_tok = rows.n;
         } else {
             x.tok0 = x.b * a.max_tokens;
             x.n_tok = a.max_tokens;

@@ -56,12 +56,9 @@ __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ App
     __shared__ float2 cs[kTokens][D / 2];
     __shared__ long long row_off[kTokens];  // element offset of the token's row in the cache
     const int b = blockIdx.x / p.tiles, t0 = (blockIdx.x % p.tiles) * kTokens;
-    int c0 = a.cu[b], c1 = a.cu[b + 1];
-    const int len = max(a.lens[b], 0);
-    c0 = max(c0, 0);
-    c1 = min(c1, a.n_tokens);
-    const int n = c1 - c0;
-    if (threadIdx.x == 0 && t0 == 0 && n > a.max_tokens) atomicOr(&g_append_error_word, kKvErrTokens);
+    const TokenRows rows = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
+    const int len = max(a.lens[b], 0), c0 = rows.first, n = rows.n;
+    if (threadIdx.x == 0 && t0 == 0 && rows.bad) atomicOr(&g_append_error_word, kKvErrTokens);
     const int nt = min(n - t0, kTokens);
     if (nt <= 0) return;
     // a unit's vectors, loaded before the places and angles are worked out

@@ -309,6 +309,29 @@ def test_indices_out_of_bounds_are_reported(ra_lib):
     run(cu=i32([-5, 1, 2]).to(DEV))
 
 
+@pytest.mark.parametrize("lens,width", [([20, 30], 1), ([20, 30], 4000), ([80, 50], 1)])
+def test_token_rows_out_of_bounds_are_reported(ra_lib, lens, width):
+    """Token rows past the tensors' or below 0, and counts above their bound or below 0, in
+    each kernel: clusters, rows (the bound on the lengths far above them), tiles."""
+    m = 40 if lens[0] == 80 else 1
+    x = Batch([m, m], lens, 16, 1, 64, seed=6, fill=0.0)
+    q, k, v = (randn(2 * m, 1, 64, seed=i).to(DEV) for i in (2, 3, 4))
+    kp, vp, lens_, tables = x.gpu("kp", "vp", "lens", "tables")
+    wide = torch.cat([tables] + [tables[:, :1]] * width, 1)
+
+    def run(cu):
+        cu = i32(cu).to(DEV)
+        ra_lib.prefix_attn_fwd(q, kp, vp, cu, lens_, wide, m)
+        first = ra_lib.load().ra_sync_status(None)
+        ra_lib.paged_kv_append(q, k, v, kp.clone(), vp.clone(), cu, lens_, tables, None, m)
+        return first, ra_lib.load().ra_sync_status(None)
+
+    assert run([0, m, 2 * m]) == (0, 0)
+    for cu in ([0, m, 2 * m + 1], [0, m, 1 << 30], [-5, m, 2 * m], [0, 2 * m, 2 * m],
+               [0, 2 * m, m], [0, m, -(1 << 31)], [-(1 << 31), (1 << 31) - 1, 2 * m]):
+        assert run(cu) == (5, 5), cu
+
+
 APPEND = [  # n, lens, page, hq, hkv, d, rot, interleaved, offset
     ([1], [1], 16, 4, 2, 64, 64, False, 0),
     ([1, 1, 1], [1, 17, 200], 16, 8, 2, 128, 128, False, 32768),
