@@ -128,9 +128,9 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Cross attention with autograd: q [B, Lq, H_q, D] to an encoder's states k, v
     [B, Lk, H_kv, D] (bf16; slices of one projection are taken as they are), per batch row
     the first kv_lens[b] of them (int32 [B], None: all) -> O [B, Lq, H_q, D] bf16.
-    backward() gives dq, dk, dv in bf16 (summed in fp32, rounded once).  A backward pass can be
-    captured into a graph while no eager graph of the same leaves is alive (torch ties a leaf
-    to the stream of the first; it raises otherwise)."""
+    backward() gives dq, dk, dv in bf16 (summed in fp32, rounded once); a second derivative
+    raises.  A backward pass can be captured into a graph while no eager graph of the same
+    leaves is alive (torch ties a leaf to the stream of the first; it raises otherwise)."""
     if q.dtype != torch.bfloat16:
         raise ValueError("the differentiable path takes bf16 inputs (the tensor-core backward)")
     if scale is None:

@@ -315,6 +315,22 @@ std::tuple<Tensor, Tensor, Tensor> cross_attn_bwd(const Tensor& q, const Tensor&
     return {dq, dk, dv};
 }
 
+// Gradients that a graph of their own is asked for (create_graph): a second derivative is
+// refused when it is taken; without this node it would silently lack this operator's part.
+// q, k and v are arguments so that the node lies on the way to them.
+struct OnceDifferentiable : torch::autograd::Function<OnceDifferentiable> {
+    static torch::autograd::variable_list forward(torch::autograd::AutogradContext*,
+                                                  const Tensor& dq, const Tensor& dk,
+                                                  const Tensor& dv, const Tensor&,
+                                                  const Tensor&, const Tensor&) {
+        return {dq.detach(), dk.detach(), dv.detach()};
+    }
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext*,
+                                                   torch::autograd::variable_list) {
+        refuse("cross_attention can be differentiated once");
+    }
+};
+
 // The forward keeps q, k, v, O (bf16), the LSE and the key counts; gradients come in bf16,
 // summed in fp32 and rounded once.
 struct CrossAttention : torch::autograd::Function<CrossAttention> {
@@ -332,6 +348,10 @@ struct CrossAttention : torch::autograd::Function<CrossAttention> {
         auto [dq, dk, dv] =
             cross_attn_bwd(s[0], s[1], s[2], s[3], s[4], grads[0].contiguous(), lens,
                            ctx->saved_data["scale"].toDouble(), at::kBFloat16, {});
+        if (at::GradMode::is_enabled()) {
+            const auto g = OnceDifferentiable::apply(dq, dk, dv, s[0], s[1], s[2]);
+            return {g[0], g[1], g[2], Tensor(), Tensor()};
+        }
         return {dq, dk, dv, Tensor(), Tensor()};
     }
 };

@@ -175,3 +175,17 @@ def test_captured_training_step(ra_lib):
         torch.cuda.synchronize()
         want = ref.cross_backward(q, kv[:, :, 0], kv[:, :, 1], lens, do, q.shape[-1] ** -0.5)
         ref.check_grads(g, want, str(seed))
+
+
+def test_second_derivative_is_refused(ra_lib):
+    """With create_graph the gradients are the same; differentiating them raises."""
+    from sequence_parallelism_attn_b200 import autograd
+    q, kv, do, _ = inputs(1, 31)
+    x = [t.to(DEV).contiguous().requires_grad_() for t in (q, kv[:, :, 0], kv[:, :, 1])]
+    plain = torch.autograd.grad(autograd.cross_attention(*x), x, do.to(DEV))
+    again = torch.autograd.grad(autograd.cross_attention(*x), x, do.to(DEV), create_graph=True)
+    # (one key tile: an element of dq is a single addition to zero)
+    assert all(torch.equal(a, b) for a, b in zip(plain, again))
+    assert not any(a.requires_grad for a in plain) and all(b.requires_grad for b in again)
+    with pytest.raises((ValueError, RuntimeError), match="differentiated once"):
+        torch.autograd.grad(sum(g.float().sum() for g in again) + (x[0] ** 2).sum(), x)
