@@ -29,6 +29,19 @@ __device__ __forceinline__ TokenRows token_rows(const int* cu, int b, int n_toke
     return r;
 }
 
+// A whole warp: the last of B sequences that starts at or before the token (0 where none does),
+// 32 ways at a time.
+__device__ __forceinline__ int find_sequence(const int* cu, int B, int tok) {
+    int b = 0, hi = B;
+    while (hi - b > 1) {
+        const int step = (hi - b + 31) / 32, e = b + (int)(threadIdx.x & 31) * step;
+        const unsigned le = __ballot_sync(0xffffffffu, e < hi && cu[e] <= tok);
+        if (le) b += (31 - __clz(le)) * step;
+        hi = min(hi, b + step);
+    }
+    return b;
+}
+
 struct AppendArgs {
     const void *q, *k, *v;
     long long q_tstride, k_tstride, v_tstride, q_out_tstride;  // elements between tokens
@@ -69,7 +82,9 @@ struct KvArgs {
 // kernels, or both by a third (kKvCluster): the tile kernel in ranges of `chunk` keys, each a partial result of its rows (two
 // where its warpgroups share a row tile), or the rows kernel, whose warps share the keys out
 // evenly among themselves.  The combine kernel joins the partials.
-constexpr int kKvNone = 0, kKvRows = 1, kKvTiles = 2, kKvCluster = 3;
+// kKvMixed (own keys): a ragged batch of long and short runs of new tokens, the rows kernel
+// for sequences of up to `few` tokens, the tile kernel for the others.
+constexpr int kKvNone = 0, kKvRows = 1, kKvTiles = 2, kKvCluster = 3, kKvMixed = 4;
 struct KvPlan {
     int kind_p, chunk_p, splits_p, tiles_p, ksplit_p, parts_p;  // the prefix
     int kind_o, chunk_o, splits_o, tiles_o, ksplit_o, parts_o;  // own keys
@@ -78,6 +93,7 @@ struct KvPlan {
     int heads_log;                // log2 of the kv heads that its warps take side by side
     int min_groups, wide_combine; // fewest key groups of a warp; eight warps join a row
     long long slots;              // its partial slots
+    int few, row_blocks_t;        // kKvMixed: (0 elsewhere); the tile kernel's row blocks, at most
     int cluster;                  // kKvCluster (own keys and prefix together): its blocks
     int direct;                   // a single part: results written without partials
     long long blocks, workspace;  // largest index of a launch (to be below 2^31), bytes

@@ -49,12 +49,13 @@ __device__ __forceinline__ Seq get_seq(const RowsParams& p, int b) {
             const TokenRows rows = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
             s.tok0 = rows.first;
             s.n_tok = min(rows.n, a.max_tokens);
+            if (p.p.few && rows.n > p.p.few) s.n_tok = 0;  // the tile kernel's
         } else {
             s.tok0 = b * a.max_tokens;
             s.n_tok = a.max_tokens;
         }
         s.len = a.lens ? min(max(a.lens[b], 0), a.max_len) : a.max_len;
-        if (p.p.kind_o != kKvRows) s.len = 0;
+        if (p.p.kind_o == kKvTiles) s.len = 0;
         s.table = a.tables ? a.tables + (long long)b * a.max_pages : nullptr;
     }
     s.groups = (s.len + KEYS - 1) / KEYS;
@@ -287,8 +288,9 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
 // row's partials are some KB in L2), so eight partials' loads are in flight at once.  Where
 // few rows have many partials each (WPR = 8), a block's eight warps share a row's partials
 // and merge their sums: 2 sequences of 16 rows behind 11705 keys, 366 partials to a row,
-// took 55 us with one warp to a row.
-template <int D, int WPR>
+// took 55 us with one warp to a row.  MIXED: each row belongs to the rows kernel or to the
+// tile kernel by its sequence's tokens; the sequence is found by a search 32 ways at a time.
+template <int D, int WPR, bool MIXED>
 __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__ RowsParams p) {
     const KvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -302,7 +304,17 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     // rows before the first sequence's and from the last one's end on stay as they are
     const int begin = a.cu ? max(a.cu[0], 0) : 0;
     const int end = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;
-    if (p.p.kind_o == kKvRows) {
+    bool few = !MIXED && p.p.kind_o == kKvRows;  // the own keys are the rows kernel's
+    if (MIXED) {
+        live = tok >= begin && tok < end;
+        if (live) {
+            b = find_sequence(a.cu, a.B, tok);
+            const TokenRows rows_b = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
+            t = tok - rows_b.first;
+            few = rows_b.n <= p.p.few;
+            live = t >= 0 && t < min(rows_b.n, a.max_tokens) && (few || !p.p.direct);
+        }
+    } else if (p.p.kind_o == kKvRows) {
         b = fdiv(i_tok, p.dtokens);
         t = i_tok - b * a.max_tokens;
         live = b < a.B;
@@ -327,7 +339,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     const float *o1 = nullptr, *o2 = nullptr, *l1 = nullptr, *l2 = nullptr;
     long long s1 = rows, s2 = rows;  // rows between a run's partials
     int len = 0;
-    if (p.p.kind_o == kKvRows) {
+    if (few) {
         len = a.lens ? a.lens[b] : a.max_len;
         if (len > a.max_len && t == 0 && head == 0 && lane == 0)
             atomicOr(&g_kv_error_word, kKvErrLength);
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         o1 = p.slot_o + ((long long)mt.x * R + r % R) * D;
         l1 = p.slot_lse + (long long)mt.x * R + r % R;
     }
-    if (p.p.kind_o == kKvTiles) {
+    if (!few) {
         n2 = p.p.parts_o;
         o2 = p.part_o + (p.p.parts_p * rows + row) * D;
         l2 = p.part_lse + p.p.parts_p * rows + row;
@@ -496,10 +508,16 @@ cudaError_t launch_rows(const RowsParams& p, unsigned grid, bool after_tiles) {
     return launch_pdl(k, p, grid, kWarps * 32, C::SMEM, p.a.stream, after_tiles);
 }
 
+template <int D>
+auto pick_combine(const KvPlan& p) {
+    if (p.few) return p.wide_combine ? kv_combine_kernel<D, 8, true> : kv_combine_kernel<D, 1, true>;
+    return p.wide_combine ? kv_combine_kernel<D, 8, false> : kv_combine_kernel<D, 1, false>;
+}
+
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // The tile kernel's share of a plan over `units` (batch rows) x H_kv heads, `tokens` tokens
-// and `keys` keys each: row blocks, and the length of a key range, by a plain model.
+// (`all_tokens` in all where the units differ, else 0) and `keys` keys each: row blocks, and the length of a key range, by a plain model.
 //   - A block costs its key tiles and three more for filling and draining, at tile_us each.
 //   - A row block's keys are cut into ranges of `per` tiles and a shorter last one; the full
 //     ranges come first in the grid, so the short ones fill up the SMs that a last wave of
@@ -510,16 +528,17 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 //     the tile kernel leaves free, at some 45 GB/s of keys to an SM, and take the others as
 //     they become free; so where the tile kernel fits in less than a wave, fewer and longer
 //     ranges can be the better choice.
-void plan_tiles(long long units, int H_kv, int group, int tokens, int keys, int D,
+void plan_tiles(long long units, int H_kv, int group, int tokens, int all_tokens, int keys, int D,
                 long long part_bytes, bool joined, double rows_bytes, int& chunk, int& splits,
                 int& blocks, int& ksplit, int& parts) {
     const int tpt = 128 / group, tiles = ceil_div(tokens, tpt);
     ksplit = tiles == 1;
     blocks = ksplit ? 1 : ceil_div(tiles, 2);
     const int kt = ceil_div(keys, 128);
-    const long long items = units * H_kv * blocks;
+    const long long items = all_tokens ? (long long)H_kv * ceil_div(all_tokens, ksplit ? tpt : 2 * tpt)
+                                       : units * H_kv * blocks;
     // (a row tile's empty warps cost nothing, a half-empty block still its MMAs)
-    const double fill = (double)tokens * group / (256.0 * blocks);
+    const double fill = all_tokens ? 1.0 : (double)tokens * group / (256.0 * blocks);
     const double tile_us = (D == 128 ? 2.2 : 1.8) * (ksplit ? 0.6 : 0.6 + 0.4 * fill);
     const double rows_sm_us = rows_bytes / 45e3;
     double best = 0;
@@ -604,7 +623,22 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
     const long long part_bytes = (long long)n_tokens * H_q * (D + 1) * 4;
     p.kind_p = prefix_len == 0 ? kKvNone : (tiles_ok && rows_p > 32 ? kKvTiles : kKvRows);
     p.kind_o = tiles_ok && rows_o > 32 ? kKvTiles : kKvRows;
-    const long long rows_most = p.kind_p == kKvRows && rows_p > rows_o ? rows_p
+    // A step of a serving loop may hold tokens of running sequences and a new prompt: where a
+    // sequence has at most 0.6 of the most tokens on average, those with few go to the rows
+    // kernel (16 rows, a fragment's; 32 where a token alone has more than 16), the others to
+    // the tile kernel, whose grid is then the row blocks that n_tokens can make, not B times
+    // the most.  Measured, us, tile kernel alone against both (32 / 8 heads of 128):
+    //   63 single tokens over 4096 keys, a prompt of 1000: 308, 200    1 and 500: 64, 36
+    //   255 single tokens over 500 keys, one of 2000: 745, 197
+    //   300, 200, 100 and 50 over 300 .. 2000 keys (0.54 of the most): 56, 55
+    //   32 of 9, 8, 7, 1 in turn over 2000 (0.69): 60, 74    16 of 100 and 200 (0.75): 102, 134
+    const int few = group <= 16 ? 16 / group : 32 / group;
+    if (p.kind_o == kKvTiles && paged && few > 0 && 5ll * n_tokens <= 3ll * B * max_tokens) {
+        p.kind_o = kKvMixed;
+        p.few = few;
+    }
+    const long long rows_most = p.kind_o == kKvMixed                       ? few * group
+                                : p.kind_p == kKvRows && rows_p > rows_o ? rows_p
                                 : p.kind_o == kKvRows                  ? rows_o
                                                                        : rows_p;
     p.mt = rows_most > 16 ? 2 : 1;
@@ -615,20 +649,30 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
         groups += (long long)ceil_div(prefix_len, group_keys(D)) * p.tiles_p * H_kv;
     } else if (p.kind_p == kKvTiles) {
         // own keys beside it: somewhat over half of their bound
-        const double own = p.kind_o == kKvRows ? 0.6 * B * (double)max_len * H_kv * D * 4 : 0.0;
-        plan_tiles(1, H_kv, group, n_tokens, prefix_len, D, part_bytes, true, own, p.chunk_p,
+        const double own = p.kind_o != kKvTiles ? 0.6 * B * (double)max_len * H_kv * D * 4 : 0.0;
+        plan_tiles(1, H_kv, group, n_tokens, 0, prefix_len, D, part_bytes, true, own, p.chunk_p,
                    p.splits_p, p.tiles_p, p.ksplit_p, p.parts_p);
     }
     if (p.kind_o == kKvRows) {
         p.tiles_o = ceil_div(rows_o, R);
         groups += (long long)B * ceil_div(max_len, group_keys(D)) * p.tiles_o * H_kv;
-    } else {
-        plan_tiles(B, H_kv, group, max_tokens, max_len, D, part_bytes, p.kind_p != kKvNone, 0.0,
+    } else if (p.kind_o == kKvTiles) {
+        plan_tiles(B, H_kv, group, max_tokens, 0, max_len, D, part_bytes, p.kind_p != kKvNone, 0.0,
                    p.chunk_o, p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
+    } else {
+        plan_tiles(B, H_kv, group, max_tokens, n_tokens, max_len, D, part_bytes,
+                   p.kind_p != kKvNone, 0.6 * B * (double)max_len * H_kv * D * 4, p.chunk_o,
+                   p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
+        // sum of ceil(n_b / block) over the sequences of more than `few` tokens
+        const int block = (p.ksplit_o ? 1 : 2) * (128 / group), most = n_tokens / (few + 1);
+        p.row_blocks_t = n_tokens / block + (B < most ? B : most);
+        p.tiles_o = 1;
+        groups += (long long)B * ceil_div(max_len, group_keys(D)) * H_kv;
     }
-    p.direct = p.kind_p == kKvNone && p.kind_o == kKvTiles && p.parts_o == 1;
+    p.direct = p.kind_p == kKvNone && p.parts_o == 1;
     p.blocks = (p.kind_p == kKvTiles ? (long long)p.splits_p * H_kv * p.tiles_p : 0) +
-               (p.kind_o == kKvTiles ? (long long)B * p.splits_o * H_kv * p.tiles_o : 0);
+               (p.kind_o == kKvTiles ? (long long)B * p.splits_o * H_kv * p.tiles_o : 0) +
+               (long long)p.row_blocks_t * p.splits_o * H_kv;
     long long bytes = p.direct ? 0 : (p.parts_p + p.parts_o) * part_bytes;
     if (groups > 0) {
         // A stretch costs its groups, every partial of a row some of the combine's time: with
@@ -651,18 +695,18 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
         // beside 2 us a block.  24 x 8 tokens of 16 heads with 16 partials: 3 us or 24 us; 32
         // rows with 366: 40 us or 5 us.
         const double steps = (double)(longest / per + 1 + p.parts_p) / 8;
-        const double narrow = ceil_div((long long)B * max_tokens * H_q, 8 * 3 * kSms) *
+        const long long rows = (p.few ? (long long)n_tokens : (long long)B * max_tokens) * H_q;
+        const double narrow = ceil_div(rows, 8 * 3 * kSms) *
                               (2.0 + 0.8 * steps);
-        const double wide = ceil_div((long long)B * max_tokens * H_q, 2 * kSms) *
+        const double wide = ceil_div(rows, 2 * kSms) *
                             (2.0 + 0.1 * steps);
         p.wide_combine = wide < narrow;
         p.heads_log = H_kv % 4 == 0 ? 2 : H_kv % 2 == 0 ? 1 : 0;
         p.j_own = p.kind_p == kKvRows ? H_kv * p.tiles_p : 0;
         const long long js =
-            p.j_own + (p.kind_o == kKvRows ? (long long)B * H_kv * p.tiles_o : 0);
+            p.j_own + (p.kind_o != kKvTiles ? (long long)B * H_kv * p.tiles_o : 0);
         p.slots = (long long)p.row_blocks * kWarps + js;
         bytes += p.slots * R * (D + 1) * 4 + js * 8 + 32;
-        const long long rows = (long long)B * max_tokens * H_q;  // the combine's, at most
         if (p.blocks < p.slots) p.blocks = p.slots;
         if (p.blocks < rows) p.blocks = rows;
         if (p.blocks < groups) p.blocks = groups;
@@ -692,7 +736,7 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
 cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wait_limit_ns,
                       const char** why) {
     cudaError_t e = cudaSuccess;
-    const bool tiled = plan.kind_p == kKvTiles || plan.kind_o == kKvTiles;
+    const bool tiled = plan.kind_p == kKvTiles || plan.kind_o == kKvTiles || plan.few;
     if (tiled) {
         e = launch_kv_tiles(a, plan, wait_limit_ns, why);
         if (e != cudaSuccess) return e;
@@ -712,9 +756,10 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
     }
     const long long rows = (long long)a.n_tokens * a.H_q;
     p.part_o = (float*)a.workspace;
-    p.part_lse = p.part_o + (long long)(plan.parts_p + plan.parts_o) * rows * a.D;
+    const int parts = plan.direct ? 0 : plan.parts_p + plan.parts_o;
+    p.part_lse = p.part_o + parts * rows * a.D;
     if (plan.row_blocks > 0) {
-        float* after = p.part_lse + (long long)(plan.parts_p + plan.parts_o) * rows;
+        float* after = p.part_lse + parts * rows;
         p.slot_o = (float*)(((uintptr_t)after + 15) & ~(uintptr_t)15);
         p.slot_lse = p.slot_o + plan.slots * 16 * plan.mt * a.D;
         p.meta = (int2*)(p.slot_lse + plan.slots * 16 * plan.mt);
@@ -732,17 +777,12 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
                 e = page16 ? launch_rows<64, 2, true>(p, grid, tiled) : launch_rows<64, 2, false>(p, grid, tiled);
         }
     }
-    if (e != cudaSuccess || plan.direct) return e;
+    if (e != cudaSuccess || (plan.direct && !plan.few)) return e;
     const long long out_rows =
         plan.kind_o == kKvRows ? (long long)a.B * a.max_tokens * a.H_q : rows;
-    if (plan.wide_combine) {
-        const unsigned cg = (unsigned)out_rows;
-        return a.D == 128 ? launch_pdl(kv_combine_kernel<128, 8>, p, cg, 256, 0, a.stream, true)
-                          : launch_pdl(kv_combine_kernel<64, 8>, p, cg, 256, 0, a.stream, true);
-    }
-    const unsigned cg = (unsigned)((out_rows + 7) / 8);
-    return a.D == 128 ? launch_pdl(kv_combine_kernel<128, 1>, p, cg, 256, 0, a.stream, true)
-                      : launch_pdl(kv_combine_kernel<64, 1>, p, cg, 256, 0, a.stream, true);
+    const unsigned cg = (unsigned)(plan.wide_combine ? out_rows : (out_rows + 7) / 8);
+    auto k = a.D == 128 ? pick_combine<128>(plan) : pick_combine<64>(plan);
+    return launch_pdl(k, p, cg, 256, 0, a.stream, true);
 }
 
 cudaError_t read_and_clear_kv_error(unsigned int* value) {

@@ -57,6 +57,7 @@ struct __align__(64) TileParams {
     int chunk_p, splits_p, blocks_p, ksplit_p, part_p;  // prefix: keys per split, ...
     int chunk_o, splits_o, blocks_o, ksplit_o, part_o;  // own keys; first partial index
     unsigned items_p;
+    int few;         // > 0: the packed form
     int direct;
     float scale_log2;
     float* parts;    // [part][token][head][D]
@@ -170,6 +171,9 @@ struct Item {
     const int* table;      // page ids, null where dense
 };
 
+// PACKED: own keys of sequences with more than `few` tokens only, their row blocks counted
+// through the batch (an instance of its own: the search costs the softmax registers).
+template <bool PACKED>
 __device__ __forceinline__ bool make_item(const TileParams& p, Item& x) {
     const KvArgs& a = p.a;
     unsigned item = blockIdx.x;
@@ -190,12 +194,64 @@ __device__ __forceinline__ bool make_item(const TileParams& p, Item& x) {
         x.part = p.part_p + split * (1 + x.ksplit);
     } else {
         item -= p.items_p;
-        blk = item % p.blocks_o;
-        item /= p.blocks_o;
-        x.g = item % a.H_kv;
-        item /= a.H_kv;
-        split = item % p.splits_o;
-        x.b = item / p.splits_o;
+        if (PACKED) {
+            // the item-th row block of the sequences with many tokens: every warp adds up
+            // their blocks; the first block's first warp looks at the whole batch, to report
+            const bool report = item == 0 && threadIdx.x < 32;
+            const int lane = threadIdx.x & 31, size = p.ksplit_o ? p.tpt : 2 * p.tpt;
+            x.g = item % a.H_kv;
+            item /= a.H_kv;
+            split = item % p.splits_o;
+            const int r = (int)(item / p.splits_o);
+            int at = 0;
+            x.b = -1;
+            blk = 0;
+#pragma unroll 1
+            for (int e0 = 0; e0 < a.B && (x.b < 0 || report); e0 += 256) {
+                int w[8], all = 0;  // 256 sequences' loads in flight at once
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int e = e0 + 32 * i + lane;
+                    w[i] = 0;
+                    if (e < a.B) {
+                        const TokenRows rows = token_rows(a.cu, e, a.n_tokens, a.max_tokens);
+                        if (rows.n > p.few) w[i] = (min(rows.n, a.max_tokens) + size - 1) / size;
+                        if (report && rows.bad)
+                            atomicOr(&g_kv_tile_error_word, kKvErrTokens << 8);
+                    }
+                    all += w[i];
+                }
+                all = __reduce_add_sync(0xffffffffu, all);
+                if (x.b >= 0 || at + all <= r) {
+                    at += all;
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int sum = __reduce_add_sync(0xffffffffu, w[i]);
+                    if (x.b < 0 && at + sum > r) {
+                        int incl = w[i];
+#pragma unroll
+                        for (int off = 1; off < 32; off <<= 1) {
+                            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                            if (lane >= off) incl += y;
+                        }
+                        const int l = __ffs(__ballot_sync(0xffffffffu, at + incl > r)) - 1;
+                        x.b = e0 + 32 * i + l;
+                        blk = r - at - __shfl_sync(0xffffffffu, incl - w[i], l);
+                    }
+                    at += sum;
+                }
+            }
+            if (x.b < 0) return false;
+        } else {
+            blk = item % p.blocks_o;
+            item /= p.blocks_o;
+            x.g = item % a.H_kv;
+            item /= a.H_kv;
+            split = item % p.splits_o;
+            x.b = item / p.splits_o;
+        }
         const bool first = threadIdx.x == 0 && split == 0;
         if (a.cu) {
             const TokenRows rows = token_rows(a.cu, x.b, a.n_tokens, a.max_tokens);
@@ -592,7 +648,7 @@ __device__ __forceinline__ void softmax_wg(const TileParams& p, uint32_t base, u
     }
 }
 
-template <int D>
+template <int D, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 1) kv_tiles_sm100(const __grid_constant__ TileParams p) {
     using C = Cfg<D>;
     Item x;
@@ -602,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_sm100(const __grid_const
         tma_prefetch_desc(&p.tm_v);
     }
     pdl_launch_dependents();  // the rows kernel, which waits for this one only at its end
-    if (!make_item(p, x)) return;  // the same for every thread of the block
+    if (!make_item<PACKED>(p, x)) return;  // the same for every thread of the block
     extern __shared__ uint8_t smem_raw[];
     uint32_t base = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (base & 1023u)) & 1023u;
@@ -691,13 +747,13 @@ bool encode(CUtensorMap* m, const void* ptr, int D, long long n1, long long n2, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool PACKED>
 cudaError_t launch(const TileParams& p, unsigned grid, const char** why) {
-    auto k = kv_tiles_sm100<D>;
+    auto k = kv_tiles_sm100<D, PACKED>;
     // the register split assumes the launch allocation: a raise beyond it would never complete
     static const int regs = [] {
         cudaFuncAttributes fa;
-        return cudaFuncGetAttributes(&fa, kv_tiles_sm100<D>) == cudaSuccess ? fa.numRegs : -1;
+        return cudaFuncGetAttributes(&fa, kv_tiles_sm100<D, PACKED>) == cudaSuccess ? fa.numRegs : -1;
     }();
     if (regs != (int)kRegsLaunch) {
         *why = "tile kernel compiled with a register count its register split does not assume";
@@ -726,7 +782,7 @@ cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& plan, unsigned long l
         while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
         if (a.page_size < kBN) p.box = a.page_size;
     }
-    const bool has_p = plan.kind_p == kKvTiles, has_o = plan.kind_o == kKvTiles;
+    const bool has_p = plan.kind_p == kKvTiles;
     p.chunk_p = plan.chunk_p;
     p.splits_p = plan.splits_p;
     p.blocks_p = plan.tiles_p;
@@ -739,7 +795,11 @@ cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& plan, unsigned long l
     p.part_o = plan.parts_p;
     p.items_p = has_p ? (unsigned)((long long)plan.splits_p * a.H_kv * plan.tiles_p) : 0;
     const long long grid =
-        p.items_p + (has_o ? (long long)a.B * plan.splits_o * a.H_kv * plan.tiles_o : 0);
+        p.items_p +
+        (plan.few ? (long long)plan.row_blocks_t
+                  : plan.kind_o == kKvTiles ? (long long)a.B * plan.tiles_o : 0) *
+            plan.splits_o * a.H_kv;
+    p.few = plan.few;
     p.direct = plan.direct;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     p.parts = (float*)a.workspace;
@@ -755,7 +815,10 @@ cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& plan, unsigned long l
         *why = "cuTensorMapEncodeTiled failed";
         return cudaErrorInvalidValue;
     }
-    return a.D == 128 ? launch<128>(p, (unsigned)grid, why) : launch<64>(p, (unsigned)grid, why);
+    const unsigned n = (unsigned)grid;
+    if (plan.few)
+        return a.D == 128 ? launch<128, true>(p, n, why) : launch<64, true>(p, n, why);
+    return a.D == 128 ? launch<128, false>(p, n, why) : launch<64, false>(p, n, why);
 }
 
 cudaError_t read_and_clear_kv_tile_error(unsigned int* value) {

@@ -98,6 +98,15 @@ PREFIX = [  # n, lens, page, hq, hkv, d, prefix
     ([2] * 37, [2 + 31 * i % 150 for i in range(37)], 16, 8, 8, 64, 0),
     ([2, 0, 1], [50, 0, 90], 3, 4, 2, 128, 100),
     ([1] * 2500, [1 + 5 * i % 23 for i in range(2500)], 16, 1, 1, 64, 5),  # many sequences
+    # long and short runs of new tokens in one batch: some behind few, some behind many rows
+    ([1, 1, 1, 100], [50, 300, 1, 100], 16, 8, 2, 128, 0),
+    ([200, 1, 0, 4, 5, 1], [230, 77, 0, 4, 300, 2000], 64, 8, 2, 64, 0),
+    ([1, 70, 16, 17, 1, 1], [20, 70, 16, 90, 1, 0], 16, 1, 1, 128, 40),
+    ([1] * 9 + [300] + [3] * 9, [40 + 50 * i for i in range(9)] + [301] + [5] * 9, 32, 14, 2, 64, 200),
+    ([2, 1, 150, 0, 1], [9, 700, 1100, 0, 33], 128, 32, 1, 128, 0),       # 32 heads per kv head
+    ([1, 129, 1, 1], [200, 129, 3, 40], 8, 24, 1, 64, 19),
+    ([1] * 40 + [66] + [1] * 40, [1 + 7 * i for i in range(40)] + [66] + [3] * 40, 16, 4, 4, 64, 0),
+    ([0] * 33 + [90] + [1] * 1200, [0] * 33 + [90] + [1 + i % 9 for i in range(1200)], 16, 2, 1, 64, 3),
 ]
 
 
@@ -175,7 +184,8 @@ def test_padded_batch_rows_stay_with_many_tokens(ra_lib):
 
 
 @pytest.mark.parametrize("n,plen", [([3, 1, 2, 1], 0), ([3, 1, 2, 1], 20000), ([40, 30, 50, 33], 0),
-                                    ([40, 30, 50, 33], 150), ([20, 20, 1, 1], 20000)])
+                                    ([40, 30, 50, 33], 150), ([20, 20, 1, 1], 20000),
+                                    ([2, 9, 1, 90], 0), ([90, 2, 120, 1], 300)])
 def test_slice_of_a_batch(ra_lib, n, plen):
     """The last two sequences of a batch, given with all of its token rows: the rows of the
     others stay as they were, in the append too, whichever kernel takes the rows."""
@@ -309,13 +319,16 @@ def test_indices_out_of_bounds_are_reported(ra_lib):
     run(cu=i32([-5, 1, 2]).to(DEV))
 
 
-@pytest.mark.parametrize("lens,width", [([20, 30], 1), ([20, 30], 4000), ([80, 50], 1)])
+@pytest.mark.parametrize("lens,width", [([20, 30], 1), ([20, 30], 4000), ([80, 50], 1),
+                                        ([80, 50, 9, 9], 1)])
 def test_token_rows_out_of_bounds_are_reported(ra_lib, lens, width):
     """Token rows past the tensors' or below 0, and counts above their bound or below 0, in
-    each kernel: clusters, rows (the bound on the lengths far above them), tiles."""
+    each kernel: clusters, rows (the bound on the lengths far above them), tiles, both."""
     m = 40 if lens[0] == 80 else 1
-    x = Batch([m, m], lens, 16, 1, 64, seed=6, fill=0.0)
-    q, k, v = (randn(2 * m, 1, 64, seed=i).to(DEV) for i in (2, 3, 4))
+    n = ([m, m] if len(lens) == 2 else [m, 1, 1, 1])
+    N = sum(n)
+    x = Batch(n, lens, 16, 1, 64, seed=6, fill=0.0)
+    q, k, v = (randn(N, 1, 64, seed=i).to(DEV) for i in (2, 3, 4))
     kp, vp, lens_, tables = x.gpu("kp", "vp", "lens", "tables")
     wide = torch.cat([tables] + [tables[:, :1]] * width, 1)
 
@@ -326,10 +339,15 @@ def test_token_rows_out_of_bounds_are_reported(ra_lib, lens, width):
         ra_lib.paged_kv_append(q, k, v, kp.clone(), vp.clone(), cu, lens_, tables, None, m)
         return first, ra_lib.load().ra_sync_status(None)
 
-    assert run([0, m, 2 * m]) == (0, 0)
-    for cu in ([0, m, 2 * m + 1], [0, m, 1 << 30], [-5, m, 2 * m], [0, 2 * m, 2 * m],
-               [0, 2 * m, m], [0, m, -(1 << 31)], [-(1 << 31), (1 << 31) - 1, 2 * m]):
+    good = x.cu.tolist()
+    assert run(good) == (0, 0)
+    for at, bad in ((-1, N + 1), (-1, 1 << 30), (-1, -(1 << 31)), (0, -5), (0, -(1 << 31)),
+                    (1, N + 7), (1, (1 << 31) - 1), (1, -1)):
+        cu = list(good)
+        cu[at] = bad
         assert run(cu) == (5, 5), cu
+    if m == 1:
+        assert run([0, 2, 2]) == (5, 5)
 
 
 APPEND = [  # n, lens, page, hq, hkv, d, rot, interleaved, offset
@@ -341,6 +359,12 @@ APPEND = [  # n, lens, page, hq, hkv, d, rot, interleaved, offset
     ([3, 4], [8, 4], 1, 7, 1, 128, 16, False, 2000000000),
     ([6], [6], 16, 4, 2, 64, 0, False, 0),
     ([130], [131], 32, 0, 3, 128, 128, False, 5),
+    # few sequences with many tokens: blocks over the rows, whatever their sequences
+    ([1] * 40 + [99] + [2] * 40, [3 + 5 * i for i in range(40)] + [99] + [2] * 40, 16, 4, 2, 64, 64,
+     False, 77),
+    ([0, 1, 301, 0, 0, 1, 3, 2], [0, 400, 311, 0, 5, 1, 3, 9], 64, 24, 8, 128, 64, True, 0),
+    ([1] * 1100 + [50], [1 + i % 3 for i in range(1100)] + [60], 5, 0, 1, 64, 32, False, 9),
+    ([50, 1, 1, 1], [50, 9, 9, 1], 16, 1, 1, 64, 16, False, 0),                      # one warp
 ]
 
 
