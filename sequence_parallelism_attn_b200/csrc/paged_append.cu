@@ -24,10 +24,11 @@ __device__ unsigned int g_append_error_word = 0;
 namespace {
 
 constexpr int kTokens = 4;  // tokens per block
+constexpr long long kNoPlace = -1, kNoToken = -2;  // of a token's row in the cache
 
 struct AppendParams {
     AppendArgs a;
-    int tiles;  // blocks per sequence
+    int tiles;  // blocks per sequence (the flat form: 0)
 };
 
 __device__ __forceinline__ void rotate2(uint32_t& xy_lo, uint32_t& xy_hi, float2 cs0, float2 cs1) {
@@ -49,18 +50,36 @@ __device__ __forceinline__ uint32_t rotate1(uint32_t xy, float2 cs) {
 
 // One thread moves two 16-byte vectors of one head: the two halves of 8 rotated pairs, or
 // neighbours.  Units of a token: (H_q + 2 H_kv) heads x D/16.
-template <int D>
+//
+// A block has up to four tokens of one sequence or, FLAT, any four rows next to each other,
+// whose sequences it looks up: B x max_tokens / 4 blocks are too many where few sequences have
+// that many tokens.
+template <int D, bool FLAT>
 __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int UPH = D / 16;
     const AppendArgs& a = p.a;
     __shared__ float2 cs[kTokens][D / 2];
     __shared__ long long row_off[kTokens];  // element offset of the token's row in the cache
-    const int b = blockIdx.x / p.tiles, t0 = (blockIdx.x % p.tiles) * kTokens;
-    const TokenRows rows = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
-    const int len = max(a.lens[b], 0), c0 = rows.first, n = rows.n;
-    if (threadIdx.x == 0 && t0 == 0 && rows.bad) atomicOr(&g_append_error_word, kKvErrTokens);
-    const int nt = min(n - t0, kTokens);
-    if (nt <= 0) return;
+    __shared__ int place[kTokens];  // FLAT: the token's place among its sequence's own keys
+    int b = 0, t0 = 0, len = 0, n = 0, row0, nt;  // row0: the first token's row
+    if (FLAT) {
+        row0 = (int)blockIdx.x * kTokens;
+        nt = min(a.n_tokens - row0, kTokens);
+        if (blockIdx.x == 0)
+            for (int e = threadIdx.x; e < a.B; e += blockDim.x)
+                if (token_rows(a.cu, e, a.n_tokens, a.max_tokens).bad)
+                    atomicOr(&g_append_error_word, kKvErrTokens);
+    } else {
+        b = blockIdx.x / p.tiles;
+        t0 = (blockIdx.x % p.tiles) * kTokens;
+        const TokenRows rows = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
+        len = max(a.lens[b], 0);
+        n = rows.n;
+        row0 = rows.first + t0;
+        if (threadIdx.x == 0 && t0 == 0 && rows.bad) atomicOr(&g_append_error_word, kKvErrTokens);
+        nt = min(n - t0, kTokens);
+        if (nt <= 0) return;
+    }
     // a unit's vectors, loaded before the places and angles are worked out
     const int units = (a.H_q + 2 * a.H_kv) * UPH, ru = a.rot / 16;
     uint4 x[kTokens], y[kTokens];
@@ -78,15 +97,15 @@ __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ App
         for (int t = 0; t < kTokens; ++t)
             if (t < nt) {
                 const uint4* r =
-                    reinterpret_cast<const uint4*>(src + (long long)(c0 + t0 + t) * stride + h * D);
+                    reinterpret_cast<const uint4*>(src + (long long)(row0 + t) * stride + h * D);
                 x[t] = r[v0];
                 y[t] = r[v1];
             }
     };
     if (threadIdx.x < units) load(threadIdx.x);
-    if (threadIdx.x < nt) {
-        const int pos = len - n + t0 + (int)threadIdx.x;
-        long long off = -1;
+    // the place of token t of the block in the cache: kNoPlace, or kNoToken where the row is none
+    auto locate = [&](int t, int b, int pos) {
+        long long off = kNoPlace;
         if (pos >= 0) {
             const int slot = pos / a.page_size;
             if (slot >= a.max_pages) {
@@ -102,12 +121,27 @@ __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ App
         } else {
             atomicOr(&g_append_error_word, kKvErrLength);
         }
-        row_off[threadIdx.x] = off;
+        row_off[t] = off;
+    };
+    if (FLAT) {
+        for (int t = threadIdx.x >> 5; t < nt; t += blockDim.x >> 5) {
+            const int tok = row0 + t, e = find_sequence(a.cu, a.B, tok);
+            const TokenRows rows = token_rows(a.cu, e, a.n_tokens, a.max_tokens);
+            const int i = tok - rows.first, pos = max(a.lens[e], 0) - rows.n + i;
+            if ((threadIdx.x & 31) == 0) {
+                place[t] = pos;
+                if (i >= 0 && i < min(rows.n, a.max_tokens)) locate(t, e, pos);
+                else row_off[t] = kNoToken;
+            }
+        }
+        __syncthreads();
+    } else if (threadIdx.x < nt) {
+        locate(threadIdx.x, b, len - n + t0 + (int)threadIdx.x);
     }
     const int half = a.rot / 2;
     for (int i = threadIdx.x; i < nt * half; i += blockDim.x) {
         const int t = i / half, j = i - t * half;
-        const double pos = (double)a.pos_offset + (double)(len - n + t0 + t);
+        const double pos = (double)a.pos_offset + (double)(FLAT ? place[t] : len - n + t0 + t);
         double turns = pos * (double)a.inv_freq[j] * 0.15915494309189533577;  // 1 / (2 pi)
         turns -= rint(turns);
         float s, c;
@@ -140,10 +174,11 @@ __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ App
                     }
                 }
                 uint4* w = nullptr;
-                if (is_q)
-                    w = reinterpret_cast<uint4*>((uint16_t*)a.q_out +
-                                                 (long long)(c0 + t0 + t) * a.q_out_tstride + h * D);
-                else if (row_off[t] >= 0)
+                if (is_q) {
+                    if (!FLAT || row_off[t] != kNoToken)
+                        w = reinterpret_cast<uint4*>((uint16_t*)a.q_out +
+                                                     (long long)(row0 + t) * a.q_out_tstride + h * D);
+                } else if (row_off[t] >= 0)
                     w = reinterpret_cast<uint4*>((uint16_t*)(is_v ? a.v_pages : a.k_pages) +
                                                  row_off[t] + h * D);
                 if (w) {
@@ -162,9 +197,21 @@ cudaError_t launch_paged_append(const AppendArgs& a) {
     p.tiles = (a.max_tokens + kTokens - 1) / kTokens;
     const int units = (a.H_q + 2 * a.H_kv) * (a.D / 16);
     const int threads = units >= 384 ? 384 : ((units + 31) / 32) * 32;
-    const unsigned grid = (unsigned)((long long)p.tiles * a.B);
-    if (a.D == 128) append_kernel<128><<<grid, threads, 0, a.stream>>>(p);
-    else append_kernel<64><<<grid, threads, 0, a.stream>>>(p);
+    unsigned grid = (unsigned)((long long)p.tiles * a.B);
+    // Flat where at least half of the blocks by sequence would be empty.  Measured, us on the GPU,
+    // by sequence and flat (32 + 2 x 8 heads of 128): 16 and 1 tokens in turn, 128 sequences, 8.2,
+    // 7.0; 1000 and 500, 8 sequences, 27.7, 33.1 (the look-up comes before a block's stores); 255
+    // single tokens and one of 2000 (128,000 blocks against 564) flat 11.8, of which 9 are memory's.
+    const long long flat = (a.n_tokens + kTokens - 1) / kTokens;
+    if ((long long)p.tiles * a.B >= 2 * (flat + a.B)) {
+        p.tiles = 0;
+        grid = (unsigned)flat;
+        if (a.D == 128) append_kernel<128, true><<<grid, threads, 0, a.stream>>>(p);
+        else append_kernel<64, true><<<grid, threads, 0, a.stream>>>(p);
+        return cudaGetLastError();
+    }
+    if (a.D == 128) append_kernel<128, false><<<grid, threads, 0, a.stream>>>(p);
+    else append_kernel<64, false><<<grid, threads, 0, a.stream>>>(p);
     return cudaGetLastError();
 }
 
