@@ -587,8 +587,8 @@ void plan_tiles(long long units, int H_kv, int group, int tokens, int all_tokens
 // 8.5 + the keys at 6 TB/s.  The cluster's time is that of the longest sequence, the rows
 // kernel's that of the whole batch (whose lengths are not known here: 0.75 of their bound), and
 // only the clusters read the prefix anew for every sequence.
-bool plan_cluster(int B, long long rows, long long rows_p, int max_len, int prefix_len, int H_kv,
-                  int D, KvPlan& p) {
+bool plan_cluster(int B, long long rows, bool tiles_p, int max_len, int prefix_len, int H_kv, int D,
+                  KvPlan& p) {
     const long long js = (long long)B * H_kv;
     int c = 8;
     while (c > 1 && js * c > (c == 8 ? 224 : c == 4 ? 272 : kBlocksPerSm * kSms)) c /= 2;
@@ -598,7 +598,7 @@ bool plan_cluster(int B, long long rows, long long rows_p, int max_len, int pref
     const double steps = 0.62 * ceil_div(go + gp, kWarps * c), read = js * (go + gp) * mb / 6.2;
     const double cluster = 4.5 + (steps > read ? steps : read);
     const double other = 8.5 + 0.75 * js * go * mb / 6.0 + H_kv * gp * mb / 6.0 +
-                         (rows_p > 32 && prefix_len > 0 ? 4.0 : 0.0);  // the tile kernel beside
+                         (tiles_p ? 4.0 : 0.0);  // the tile kernel beside, for the prefix
     if (cluster > other) return false;
     p = KvPlan{};
     p.kind_o = kKvCluster;
@@ -615,14 +615,28 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
     KvPlan p = {};
     const int group = H_q / H_kv;
     const long long rows_o = (long long)max_tokens * group, rows_p = (long long)n_tokens * group;
-    if (rows_o <= 32 && plan_cluster(B, rows_o, rows_p, max_len, prefix_len, H_kv, D, p))
-        return p;
     // the tile kernel takes whole groups of heads, and pages that divide its 128-key tiles
     const bool tiles_ok =
         group <= 128 && (!paged || (page_size >= 8 && (page_size & (page_size - 1)) == 0));
+    // The most rows to leave to mma.sync: 32, but over many keys at D = 128 only 16, where a
+    // second fragment makes products and softmax the bound.  Measured, us, 8 tokens of 4 heads to
+    // a kv head (8 of 128), rows kernel or clusters against the tile kernel:
+    //   1 sequence: 2000 keys 13.8, 13.6    8000 keys 23.7, 17.1
+    //   8:  300 keys 14.2, 11.5    2000 keys 24.3, 17.7    8000 keys 77.7, 48.6
+    //   32: 300 keys 20.6, 25.3    2000 keys 84.1, 60.2    8000 keys 234, 199
+    // and 4 sequences of 8 rows behind a prefix: 8000 keys 25.0, 18.8    64000 keys 75.5, 55.0.
+    // At D = 64 (4 tokens of 8 heads to a kv head, 4 of them) 32 sequences over 8000 keys 63, 87.
+    auto most_rows = [&](int keys) { return tiles_ok && D == 128 && keys >= 1024 ? 16 : 32; };
+    const bool many = rows_o > most_rows(max_len);
+    if (!many && rows_o <= 32 &&
+        plan_cluster(B, rows_o, prefix_len > 0 && rows_p > most_rows(prefix_len), max_len,
+                     prefix_len, H_kv, D, p))
+        return p;
     const long long part_bytes = (long long)n_tokens * H_q * (D + 1) * 4;
-    p.kind_p = prefix_len == 0 ? kKvNone : (tiles_ok && rows_p > 32 ? kKvTiles : kKvRows);
-    p.kind_o = tiles_ok && rows_o > 32 ? kKvTiles : kKvRows;
+    p.kind_p = prefix_len == 0                                             ? kKvNone
+               : tiles_ok && (many || rows_p > most_rows(prefix_len)) ? kKvTiles
+                                                                           : kKvRows;
+    p.kind_o = tiles_ok && many ? kKvTiles : kKvRows;
     // A step of a serving loop may hold tokens of running sequences and a new prompt: where a
     // sequence has at most 0.6 of the most tokens on average, those with few go to the rows
     // kernel (16 rows, a fragment's; 32 where a token alone has more than 16), the others to
@@ -633,7 +647,8 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
     //   300, 200, 100 and 50 over 300 .. 2000 keys (0.54 of the most): 56, 55
     //   32 of 9, 8, 7, 1 in turn over 2000 (0.69): 60, 74    16 of 100 and 200 (0.75): 102, 134
     const int few = group <= 16 ? 16 / group : 32 / group;
-    if (p.kind_o == kKvTiles && paged && few > 0 && 5ll * n_tokens <= 3ll * B * max_tokens) {
+    if (p.kind_o == kKvTiles && paged && few > 0 && few < max_tokens &&
+        5ll * n_tokens <= 3ll * B * max_tokens) {
         p.kind_o = kKvMixed;
         p.few = few;
     }

@@ -98,6 +98,13 @@ PREFIX = [  # n, lens, page, hq, hkv, d, prefix
     ([2] * 37, [2 + 31 * i % 150 for i in range(37)], 16, 8, 8, 64, 0),
     ([2, 0, 1], [50, 0, 90], 3, 4, 2, 128, 100),
     ([1] * 2500, [1 + 5 * i % 23 for i in range(2500)], 16, 1, 1, 64, 5),  # many sequences
+    # 17 to 32 rows over many keys: the tile kernel at D = 128, for own keys, the prefix, or both
+    ([8, 8], [1500, 8], 64, 8, 2, 128, 0),
+    ([5, 6, 5], [1030, 40, 5], 16, 8, 2, 128, 11),
+    ([1, 1, 1], [40, 3, 200], 16, 16, 2, 128, 33000),
+    ([20], [1025], 16, 2, 2, 128, 0),
+    ([8, 1, 1, 1], [1200, 30, 0, 1100], 16, 8, 2, 128, 70),
+    ([6, 6], [1100, 1030], 5, 8, 2, 128, 17),
     # long and short runs of new tokens in one batch: some behind few, some behind many rows
     ([1, 1, 1, 100], [50, 300, 1, 100], 16, 8, 2, 128, 0),
     ([200, 1, 0, 4, 5, 1], [230, 77, 0, 4, 300, 2000], 64, 8, 2, 64, 0),
