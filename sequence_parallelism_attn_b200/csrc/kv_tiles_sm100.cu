@@ -17,11 +17,12 @@
 // u / 2, or u where the warpgroups share a row tile), the MMA thread issues
 //   S(0), S(1), then for every u:  S(u + 2) once S(u + 1) was read,  PV(u) once P(u) is there
 // with one score buffer, two P and two O regions.  What bounds it: with two full row tiles
-// the softmax and the tensor core (256 rows x 4 D flops per 4 D bytes): a key tile takes 2.3
-// us at D = 128 and 1.86 us at D = 64, where one row to a thread leaves the softmax's latency
+// the softmax and the tensor core (256 rows x 4 D flops per 4 D bytes): a key tile takes 2.5
+// us at D = 128 and 1.93 us at D = 64, where one row to a thread leaves the softmax's latency
 // in sight (MUFU 34%, issue slots 29% busy); a block costs some 6 us beside its key tiles.
 // Below 128 rows the rate at which K and V arrive.  1000 tokens of 32 heads behind 16384 keys
-// of 8 heads of 128: 290 us, 930 TFLOP/s, at the power cap.
+// of 8 heads of 128: 310 us, 870 TFLOP/s, at the power cap.  Of 168 registers at launch, 60
+// bytes at most are spilled (make_item's; the packed form's search most of all).
 //
 // Every wait is bounded, as in attn_sm100.cu.
 #include <cuda.h>
@@ -476,12 +477,12 @@ __device__ __forceinline__ void softmax_wg(const TileParams& p, uint32_t base, u
     const float sl2 = p.scale_log2;
     const int cnt = x.ksplit ? (x.n - wg + 1) / 2 : x.n;
 
-    // l_run: sum of the fp32 weights, which gives the LSE and divides O.  The weights that
-    // meet V are rounded to bf16, an error of half a step each whose signs are unrelated; a
-    // sum of the rounded ones to divide by would only take out their common part, for a
-    // quarter of the loop's instructions (the loop is what bounds the kernel).  The largest
-    // weight of a fresh maximum is 1, which is not rounded at all.
-    float m_run = -INFINITY, l_run = 0.f;
+    // l_run: sum of the fp32 weights, which gives the LSE.  l_used: sum of the weights as they
+    // meet V, rounded to bf16, which divides O, so that the weights applied add up to one.  With
+    // l_run for both, a quarter of the loop's instructions would go, but where a key takes most
+    // of the weight (256 times the others' at most while the maximum lags), or values are much
+    // alike, O would be off by that weight's own rounding, 2^-9 instead of the sums' 2^-13.
+    float m_run = -INFINITY, l_run = 0.f, l_used = 0.f;
     bool ok = true;
     for (int i = 0; i < cnt; ++i) {
         if (!wait_warp(bar(C::bar_sf(wg)), i & 1, abort_flag, lim, kErrSoftmax)) {
@@ -548,16 +549,16 @@ __device__ __forceinline__ void softmax_wg(const TileParams& p, uint32_t base, u
         }
         const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
         const uint64_t sl2x2 = f2_pack(sl2, sl2), negm_x2 = f2_pack(neg_m, neg_m);
-        uint64_t sum_a = 0, sum_b = 0;  // (0.f, 0.f) pairs
+        uint64_t sum_a = 0, sum_b = 0, used_a = 0, used_b = 0;  // (0.f, 0.f) pairs
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t pk[32];
 #pragma unroll
             for (int c2 = 0; c2 < 32; ++c2) {
                 if (c2 & 1)
-                    pk[c2] = softmax_pair_fp32(s2[half * 32 + c2], sl2x2, negm_x2, sum_b);
+                    pk[c2] = softmax_pair(s2[half * 32 + c2], sl2x2, negm_x2, sum_b, used_b);
                 else
-                    pk[c2] = softmax_pair_fp32(s2[half * 32 + c2], sl2x2, negm_x2, sum_a);
+                    pk[c2] = softmax_pair(s2[half * 32 + c2], sl2x2, negm_x2, sum_a, used_a);
             }
             if (half == 0 && i > 0) {  // P(i-1) there has been read by PV(i-1)
                 if (!wait_warp(bar(C::bar_pvd(wg)), (i - 1) & 1, abort_flag, lim, kErrSoftmax)) {
@@ -570,9 +571,11 @@ __device__ __forceinline__ void softmax_wg(const TileParams& p, uint32_t base, u
             tmem_st32(tP + half * 32, pk);
         }
         if (!ok) break;
-        float s0, s1;
+        float s0, s1, u0, u1;
         f2_unpack(f2_add(sum_a, sum_b), s0, s1);
+        f2_unpack(f2_add(used_a, used_b), u0, u1);
         l_run = l_run * alpha + (s0 + s1);
+        l_used = l_used * alpha + (u0 + u1);
         if (__any_sync(FULL, resc)) {
 #pragma unroll
             for (int cb = 0; cb < D / 32; ++cb) {
@@ -594,7 +597,7 @@ __device__ __forceinline__ void softmax_wg(const TileParams& p, uint32_t base, u
     tc_fence_after();
 
     // no key seen: l = 0; a NaN score comes through as a NaN sum
-    const float inv_l = l_run == 0.f ? 0.f : 1.f / l_run;
+    const float inv_l = l_used == 0.f ? 0.f : 1.f / l_used;
     const float lse2 = l_run == 0.f ? -INFINITY
                                     : (m_run == -INFINITY ? 0.f : m_run) + lg2_approx(l_run);
     const int head = x.g * p.group + hh;

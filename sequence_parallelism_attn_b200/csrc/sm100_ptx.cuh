@@ -311,24 +311,6 @@ __device__ __forceinline__ uint32_t softmax_pair(uint64_t s2, uint64_t scale2, u
     return pp;
 }
 
-
-// The same without the sum of the bf16 values (a quarter of the step's instructions).
-__device__ __forceinline__ uint32_t softmax_pair_fp32(uint64_t s2, uint64_t scale2, uint64_t negm2,
-                                                      uint64_t& sum) {
-    uint32_t pp;
-    asm("{\n\t.reg .b32 x0, x1, p0, p1;\n\t.reg .b64 x, p;\n\t"
-        "fma.rn.f32x2 x, %2, %3, %4;\n\t"
-        "mov.b64 {x0, x1}, x;\n\t"
-        "ex2.approx.ftz.f32 p0, x0;\n\t"
-        "ex2.approx.ftz.f32 p1, x1;\n\t"
-        "cvt.rn.bf16x2.f32 %0, p1, p0;\n\t"
-        "mov.b64 p, {p0, p1};\n\t"
-        "add.rn.f32x2 %1, %1, p;\n\t}"
-        : "=r"(pp), "+l"(sum)
-        : "l"(s2), "l"(scale2), "l"(negm2));
-    return pp;
-}
-
 // ------------------------------------------------------------------ register split
 // Per-warpgroup register budget change (all 4 warps of the warpgroup execute it).  The
 // sum over the block must stay within what the block was launched with.
