@@ -92,6 +92,7 @@ struct KvPlan {
     int row_blocks, j_own;        // its grid; index of the first (sequence, head, tile)
     int heads_log;                // log2 of the kv heads that its warps take side by side
     int min_groups, wide_combine; // fewest key groups of a warp; eight warps join a row
+    int packed, search;           // its row tiles counted by token rows; the combine's rows too
     long long slots;              // its partial slots
     int few, row_blocks_t;        // kKvMixed: (0 elsewhere); the tile kernel's row blocks, at most
     int cluster;                  // kKvCluster (own keys and prefix together): its blocks

@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
     auto slot_of = [&]() {
         const int jq = x.s.b < 0 ? x.g * p.p.tiles_p + x.tile
                                  : (p.p.j_own >> hl) +
-                                       (x.s.b * (a.H_kv >> hl) + x.g) * p.p.tiles_o + x.tile;
+                                       first_tile(p, x.s.b, x.s.tok0) * (a.H_kv >> hl) +
+                                       x.g * x.s.tiles + x.tile;
         return hs * ((int)p.p.slots >> hl) + wid + jq;
     };
     for (int i = 1 - C::STAGES; i < cnt; ++i) {
@@ -227,7 +228,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
                 const unsigned last = (f0 + i + x.s.groups - 1) / per;
                 const int g = (x.g << hl) + hs;
                 const int j = x.s.b < 0 ? g * p.p.tiles_p + x.tile
-                                        : p.p.j_own + (x.s.b * a.H_kv + g) * p.p.tiles_o + x.tile;
+                                        : p.p.j_own + first_tile(p, x.s.b, x.s.tok0) * a.H_kv +
+                                              g * x.s.tiles + x.tile;
                 p.meta[j] = make_int2(slot_of(), (int)last - wid + 1);
             }
         }
@@ -288,9 +290,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(cons
 // row's partials are some KB in L2), so eight partials' loads are in flight at once.  Where
 // few rows have many partials each (WPR = 8), a block's eight warps share a row's partials
 // and merge their sums: 2 sequences of 16 rows behind 11705 keys, 366 partials to a row,
-// took 55 us with one warp to a row.  MIXED: each row belongs to the rows kernel or to the
-// tile kernel by its sequence's tokens; the sequence is found by a search 32 ways at a time.
-template <int D, int WPR, bool MIXED>
+// took 55 us with one warp to a row.  SEARCH: a row's sequence is found by a search 32 ways at
+// a time: of a mixed batch, whose rows belong to the rows kernel or to the tile kernel by their
+// sequence's tokens, and of a ragged one, where B x the most tokens are far more than the rows.
+template <int D, int WPR, bool SEARCH>
 __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__ RowsParams p) {
     const KvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,15 +307,22 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
     // rows before the first sequence's and from the last one's end on stay as they are
     const int begin = a.cu ? max(a.cu[0], 0) : 0;
     const int end = a.cu ? min(a.cu[a.B], a.n_tokens) : a.n_tokens;
-    bool few = !MIXED && p.p.kind_o == kKvRows;  // the own keys are the rows kernel's
-    if (MIXED) {
+    bool few = !SEARCH && p.p.kind_o == kKvRows;  // the own keys are the rows kernel's
+    int n_tok = a.max_tokens, first_tok = tok;    // (few) the sequence's tokens, its first row
+    if (SEARCH) {
+        if (!p.p.few && blockIdx.x == 0 && warp == 0)  // (a mixed batch: the tile kernel reports)
+            for (int e = lane; e < a.B; e += 32)
+                if (token_rows(a.cu, e, a.n_tokens, a.max_tokens).bad)
+                    atomicOr(&g_kv_error_word, kKvErrTokens);
         live = tok >= begin && tok < end;
         if (live) {
             b = find_sequence(a.cu, a.B, tok);
             const TokenRows rows_b = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
-            t = tok - rows_b.first;
-            few = rows_b.n <= p.p.few;
-            live = t >= 0 && t < min(rows_b.n, a.max_tokens) && (few || !p.p.direct);
+            first_tok = rows_b.first;
+            n_tok = min(rows_b.n, a.max_tokens);
+            t = tok - first_tok;
+            few = !p.p.few || rows_b.n <= p.p.few;
+            live = t >= 0 && t < n_tok && (few || !p.p.direct);
         }
     } else if (p.p.kind_o == kKvRows) {
         b = fdiv(i_tok, p.dtokens);
@@ -322,8 +332,12 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
             const TokenRows rows_b = token_rows(a.cu, b, a.n_tokens, a.max_tokens);
             if (rows_b.bad && t == 0 && head == 0 && lane == 0)
                 atomicOr(&g_kv_error_word, kKvErrTokens);
-            tok = rows_b.first + t;
+            first_tok = rows_b.first;
+            n_tok = min(rows_b.n, a.max_tokens);
+            tok = first_tok + t;
             live = t < rows_b.n && tok < end;
+        } else {
+            first_tok = b * a.max_tokens;
         }
     } else {
         live = tok >= begin && tok < end;
@@ -369,7 +383,8 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(const __grid_constant__
         l2 = p.part_lse + p.p.parts_p * rows + row;
     } else if (len > 0) {
         const int r = t * p.group + hh;
-        const int2 mt = slots_of(p.p.j_own + (b * a.H_kv + g) * p.p.tiles_o + r / R);
+        const int2 mt = slots_of(p.p.j_own + first_tile(p, b, first_tok) * a.H_kv +
+                                 g * ((n_tok * p.group + R - 1) / R) + r / R);
         n2 = mt.y;
         s2 = R;
         o2 = p.slot_o + ((long long)mt.x * R + r % R) * D;
@@ -510,7 +525,8 @@ cudaError_t launch_rows(const RowsParams& p, unsigned grid, bool after_tiles) {
 
 template <int D>
 auto pick_combine(const KvPlan& p) {
-    if (p.few) return p.wide_combine ? kv_combine_kernel<D, 8, true> : kv_combine_kernel<D, 1, true>;
+    if (p.search)
+        return p.wide_combine ? kv_combine_kernel<D, 8, true> : kv_combine_kernel<D, 1, true>;
     return p.wide_combine ? kv_combine_kernel<D, 8, false> : kv_combine_kernel<D, 1, false>;
 }
 
@@ -658,7 +674,9 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
                                                                        : rows_p;
     p.mt = rows_most > 16 ? 2 : 1;
     const int R = 16 * p.mt;
-    long long groups = 0;  // the rows kernel's work, at most
+    long long groups = 0;   // the rows kernel's work, at most
+    long long tiles_b = 0;  // its row tiles of the sequences, of a kv head, at most
+    const long long some = B < n_tokens ? B : n_tokens;  // sequences with tokens, at most
     if (p.kind_p == kKvRows) {
         p.tiles_p = ceil_div(rows_p, R);
         groups += (long long)ceil_div(prefix_len, group_keys(D)) * p.tiles_p * H_kv;
@@ -670,7 +688,12 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
     }
     if (p.kind_o == kKvRows) {
         p.tiles_o = ceil_div(rows_o, R);
-        groups += (long long)B * ceil_div(max_len, group_keys(D)) * p.tiles_o * H_kv;
+        tiles_b = some * p.tiles_o;
+        if (tiles_b > rows_p / R + some) {
+            p.packed = 1;
+            tiles_b = rows_p / R + some;
+        }
+        groups += tiles_b * ceil_div(max_len, group_keys(D)) * H_kv;
     } else if (p.kind_o == kKvTiles) {
         plan_tiles(B, H_kv, group, max_tokens, 0, max_len, D, part_bytes, p.kind_p != kKvNone, 0.0,
                    p.chunk_o, p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
@@ -682,7 +705,8 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
         const int block = (p.ksplit_o ? 1 : 2) * (128 / group), most = n_tokens / (few + 1);
         p.row_blocks_t = n_tokens / block + (B < most ? B : most);
         p.tiles_o = 1;
-        groups += (long long)B * ceil_div(max_len, group_keys(D)) * H_kv;
+        tiles_b = some;
+        groups += tiles_b * ceil_div(max_len, group_keys(D)) * H_kv;
     }
     p.direct = p.kind_p == kKvNone && p.parts_o == 1;
     p.blocks = (p.kind_p == kKvTiles ? (long long)p.splits_p * H_kv * p.tiles_p : 0) +
@@ -710,7 +734,9 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
         // beside 2 us a block.  24 x 8 tokens of 16 heads with 16 partials: 3 us or 24 us; 32
         // rows with 366: 40 us or 5 us.
         const double steps = (double)(longest / per + 1 + p.parts_p) / 8;
-        const long long rows = (p.few ? (long long)n_tokens : (long long)B * max_tokens) * H_q;
+        // by token rows where at least half of the rows by sequence would be none's
+        p.search = p.few > 0 || (paged && 2ll * n_tokens <= (long long)B * max_tokens);
+        const long long rows = (p.search ? (long long)n_tokens : (long long)B * max_tokens) * H_q;
         const double narrow = ceil_div(rows, 8 * 3 * kSms) *
                               (2.0 + 0.8 * steps);
         const double wide = ceil_div(rows, 2 * kSms) *
@@ -718,8 +744,7 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
         p.wide_combine = wide < narrow;
         p.heads_log = H_kv % 4 == 0 ? 2 : H_kv % 2 == 0 ? 1 : 0;
         p.j_own = p.kind_p == kKvRows ? H_kv * p.tiles_p : 0;
-        const long long js =
-            p.j_own + (p.kind_o != kKvTiles ? (long long)B * H_kv * p.tiles_o : 0);
+        const long long js = p.j_own + tiles_b * H_kv;
         p.slots = (long long)p.row_blocks * kWarps + js;
         bytes += p.slots * R * (D + 1) * 4 + js * 8 + 32;
         if (p.blocks < p.slots) p.blocks = p.slots;
@@ -794,7 +819,7 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
     }
     if (e != cudaSuccess || (plan.direct && !plan.few)) return e;
     const long long out_rows =
-        plan.kind_o == kKvRows ? (long long)a.B * a.max_tokens * a.H_q : rows;
+        plan.kind_o == kKvRows && !plan.search ? (long long)a.B * a.max_tokens * a.H_q : rows;
     const unsigned cg = (unsigned)(plan.wide_combine ? out_rows : (out_rows + 7) / 8);
     auto k = a.D == 128 ? pick_combine<128>(plan) : pick_combine<64>(plan);
     return launch_pdl(k, p, cg, 256, 0, a.stream, true);

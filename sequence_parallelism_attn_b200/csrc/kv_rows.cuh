@@ -89,6 +89,16 @@ struct Seq {
     const int* table;
 };
 
+// Where the rows kernel's row tiles of sequence b (first token row: first) start, of each kv
+// head's in the batch: b times the most that a sequence has or, packed, by the token rows before
+// (a sequence's tiles hold its rows and start at most one tile behind the last one's end), so
+// that their number follows the batch's tokens and not B times the longest run.  Sequences
+// without tokens need none: min(b, first) of those before have some, at most.
+__device__ __forceinline__ int first_tile(const RowsParams& p, int b, int first) {
+    const int before = min(b, first);
+    return p.p.packed ? first * p.group / (16 * p.p.mt) + before : before * p.p.tiles_o;
+}
+
 // A warp's rows: their Q fragments, how far each sees, and the running softmax state.  Lane l
 // holds rows l/4 and l/4 + 8 of each 16-row fragment, columns 2 (l % 4) and the next of every 8.
 template <int D, int MT>

@@ -131,6 +131,75 @@ def test_prefix_attention(ra_lib, case, out_dtype):
     ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), f"case {case}")
 
 
+RAGGED = [  # one or a few long runs of new tokens among short ones, where the rows kernel takes all
+    ([1] * 20 + [150] + [1] * 7, [30 + i for i in range(20)] + [170] + [9] * 7, 24, 8, 2, 64, 0),
+    ([0, 1, 90, 0, 2, 61, 0, 0, 1], [0, 700, 90, 0, 2, 100, 5, 0, 1], 5, 4, 4, 128, 31),
+    ([1] * 300 + [77], [1 + i % 40 for i in range(300)] + [99], 48, 2, 1, 128, 50),
+    ([2, 1, 1, 33, 1], [40, 3, 1000, 40, 1], 16, 130, 1, 64, 20),
+    ([1, 1, 1, 9, 1, 1, 1, 1], [2000, 3, 1500, 9, 1, 0, 4000, 700], 64, 2, 2, 64, 0),  # one tile each
+]
+
+
+@pytest.mark.parametrize("case", range(len(RAGGED)))
+@pytest.mark.parametrize("width", [1, 3000])
+def test_ragged_batches_of_the_rows_kernel(ra_lib, case, width):
+    """Row tiles and the combine's rows counted by token rows; rows of no sequence, before the
+    first and behind the last, stay."""
+    n, lens, page, hq, hkv, d, plen = RAGGED[case]
+    x = Batch([3] + n, [3] + lens, page, hkv, d, plen, seed=7 * case, extra_rows=2)
+    q = randn(x.N, hq, d, seed=case)
+    q[:3] = q[-2:] = NAN
+    wide = torch.cat([x.tables, torch.full((len(lens) + 1, width), 1 << 29, dtype=torch.int32)], 1)
+    o = torch.full((x.N, hq, d), 7.0, device=DEV)
+    l = torch.full((hq, x.N), 7.0, device=DEV)
+    kp, vp, cu, lens_, pt = x.gpu("kp", "vp", "cu", "lens", "ptable")
+    ra_lib.prefix_attn_fwd(q.to(DEV), kp, vp, cu[1:].clone(), lens_[1:].clone(),
+                           wide[1:].contiguous().to(DEV), max(n), prefix_table=pt, prefix_len=plen,
+                           out=o, lse=l)
+    assert ra_lib.ra_sync_status() == 0
+    for rows in (slice(0, 3), slice(x.N - 2, None)):
+        assert (o[rows] == 7).all() and (l[:, rows] == 7).all()
+    want = ref.prefix_attention(q[:-2], x.kp, x.vp, x.cu[1:], x.lens[1:], x.tables[1:], x.ptable,
+                                plen, d ** -0.5)
+    ref.check_attention(o[3:-2], l[:, 3:-2].t(), (want[0][3:], want[1][3:], want[2].t()[3:]),
+                        f"case {case}")
+
+
+def test_prompt_among_single_tokens_over_odd_pages(ra_lib):
+    """255 single tokens and a prompt of 2000 whose tables could hold half a million keys: by
+    B times the longest run that is a line of 4e9 groups of keys and was refused."""
+    n, lens = [1] * 255 + [2000], [1 + 7 * i % 90 for i in range(255)] + [2000]
+    x = Batch(n, lens, 24, 2, 128, seed=3, fill=0.0)
+    wide = torch.zeros(256, 21846, dtype=torch.int32)
+    wide[:, :x.max_pages] = x.tables.clamp(max=x.n_pages - 1)
+    q = randn(x.N, 8, 128, seed=1)
+    kp, vp, cu, lens_ = x.gpu("kp", "vp", "cu", "lens")
+    o, l = ra_lib.prefix_attn_fwd(q.to(DEV), kp, vp, cu, lens_, wide.to(DEV), 2000)
+    assert ra_lib.ra_sync_status() == 0
+    want = ref.prefix_attention(q, x.kp, x.vp, x.cu, x.lens, x.tables, x.ptable, 0, 128 ** -0.5)
+    ref.check_attention(o, l.t(), (want[0], want[1], want[2].t()), "prompt")
+
+
+def test_ragged_token_rows_out_of_bounds_are_reported(ra_lib):
+    """As below, where the combine finds the sequences and nobody else looks at them all."""
+    x = Batch([1, 1, 40, 1, 1, 1], [9, 30, 60, 1, 5, 9], 24, 1, 64, seed=6, fill=0.0)
+    q = randn(x.N, 1, 64, seed=2).to(DEV)
+    kp, vp, lens_, tables = x.gpu("kp", "vp", "lens", "tables")
+
+    def run(cu):
+        ra_lib.prefix_attn_fwd(q, kp, vp, i32(cu).to(DEV), lens_, tables, 40)
+        return ra_lib.load().ra_sync_status(None)
+
+    good = x.cu.tolist()
+    assert run(good) == 0
+    for at, bad in ((-1, x.N + 1), (-1, 1 << 30), (-1, -(1 << 31)), (0, -5), (0, -(1 << 31)),
+                    (1, x.N + 7), (1, (1 << 31) - 1), (1, -1)):
+        cu = list(good)
+        cu[at] = bad
+        assert run(cu) == 5, cu
+    assert run([0, x.N, 0, x.N, 0, x.N, 0]) == 5 and run(good) == 0
+
+
 @pytest.mark.parametrize("n,lens", [([1, 1], [20, 3]), ([1] * 40, [9] * 40), ([70, 2], [75, 9])])
 def test_bounds_far_above_the_lengths(ra_lib, n, lens):
     """Without max_len the tables' capacity is the bound: far above the lengths here, which

@@ -90,6 +90,26 @@ def test_workspace_sizes(lib):
     assert lib.ra_cross_attn_workspace(1, 1, 1000, 8, 2, 64) == 0
 
 
+def test_workspace_follows_the_tokens(lib):
+    """A ragged batch of one long run of new tokens among many single ones: the workspace is in
+    proportion to the rows, whatever the page size, not to B times the longest run."""
+    def size(*a):
+        return lib.ra_prefix_attn_workspace(*a)
+
+    for B, new, hq, hkv, d in ((256, 2000, 32, 8, 128), (256, 8000, 32, 8, 128),
+                               (65, 4000, 32, 8, 128), (256, 2000, 8, 8, 64)):
+        n = B - 1 + new
+        # a row's partial result, of whole tiles of 32 rows: those that n tokens fill, one more
+        # to a sequence, one to each of the 1184 resident warps
+        tiles = n * (hq // hkv) // 32 + B + 1184 // hkv + 1
+        most = tiles * hkv * (32 * (d + 1) * 4 + 8) + 32
+        for page in (1, 5, 24, 48, 96):
+            assert 0 < size(B, n, new, new, 0, hq, hkv, d, page) <= most, (B, new, page)
+            assert size(B, n, new, 1 << 17, 0, hq, hkv, d, page) <= most, (B, new, page)
+    # sequences without tokens cost nothing
+    assert size(1 << 16, 10, 1, 4000, 0, 32, 8, 128, 16) <= size(1 << 4, 10, 1, 4000, 0, 32, 8, 128, 16)
+
+
 def test_binding_refusals():
     """The binding checks shapes, types and layouts before the library is called."""
     from sequence_parallelism_attn_b200 import ra
