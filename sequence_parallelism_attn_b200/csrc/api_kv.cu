@@ -211,9 +211,9 @@ ra_status ra_prefix_attn_fwd(const void* q, long long q_tstride, const void* k_p
     a.stream = (cudaStream_t)stream;
     const ra::KvPlan plan =
         ra::plan_kv(B, n_tokens, max_tokens, max_len, prefix_len, H_q, H_kv, D, 1, page_size);
-    RA_CHECK(check_workspace(workspace, workspace_bytes, plan.workspace));
     if ((long long)n_tokens * H_q > 0x7fffffffLL || plan.blocks > 0x7fffffffLL)
         return fail(RA_ERR_INVALID, "problem too large for one launch");
+    RA_CHECK(check_workspace(workspace, workspace_bytes, plan.workspace));
     const char* why = "prefix attention launch";
     const cudaError_t e = ra::launch_kv(a, plan, ra::wait_limit_ns(), &why);
     return e == cudaSuccess ? RA_OK : cuda_fail(e, why);

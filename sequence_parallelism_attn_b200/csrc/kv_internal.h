@@ -94,7 +94,8 @@ struct KvPlan {
     int min_groups, wide_combine; // fewest key groups of a warp; eight warps join a row
     int packed, search;           // its row tiles counted by token rows; the combine's rows too
     long long slots;              // its partial slots
-    int few, row_blocks_t;        // kKvMixed: (0 elsewhere); the tile kernel's row blocks, at most
+    int few;                      // kKvMixed (0 elsewhere)
+    int row_blocks_t;             // packed own keys of the tile kernel: its row blocks, at most
     int cluster;                  // kKvCluster (own keys and prefix together): its blocks
     int direct;                   // a single part: results written without partials
     long long blocks, workspace;  // largest index of a launch (to be below 2^31), bytes

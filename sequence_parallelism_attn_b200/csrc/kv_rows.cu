@@ -662,11 +662,16 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
     //   255 single tokens over 500 keys, one of 2000: 745, 197
     //   300, 200, 100 and 50 over 300 .. 2000 keys (0.54 of the most): 56, 55
     //   32 of 9, 8, 7, 1 in turn over 2000 (0.69): 60, 74    16 of 100 and 200 (0.75): 102, 134
+    // With more than 32 heads to a kv head a single token is the tile kernel's too: it takes all,
+    // packed (255 single tokens over 500 keys and one of 2000, 64 heads on one of
+    // 128: 1129 us by B times the most blocks, packed 168).
     const int few = group <= 16 ? 16 / group : 32 / group;
-    if (p.kind_o == kKvTiles && paged && few > 0 && few < max_tokens &&
+    bool packed = false;
+    if (p.kind_o == kKvTiles && paged && few < max_tokens &&
         5ll * n_tokens <= 3ll * B * max_tokens) {
-        p.kind_o = kKvMixed;
+        packed = true;
         p.few = few;
+        if (few > 0) p.kind_o = kKvMixed;
     }
     const long long rows_most = p.kind_o == kKvMixed                       ? few * group
                                 : p.kind_p == kKvRows && rows_p > rows_o ? rows_p
@@ -694,23 +699,24 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
             tiles_b = rows_p / R + some;
         }
         groups += tiles_b * ceil_div(max_len, group_keys(D)) * H_kv;
-    } else if (p.kind_o == kKvTiles) {
+    } else if (!packed) {
         plan_tiles(B, H_kv, group, max_tokens, 0, max_len, D, part_bytes, p.kind_p != kKvNone, 0.0,
                    p.chunk_o, p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
     } else {
+        const double own = few > 0 ? 0.6 * B * (double)max_len * H_kv * D * 4 : 0.0;
         plan_tiles(B, H_kv, group, max_tokens, n_tokens, max_len, D, part_bytes,
-                   p.kind_p != kKvNone, 0.6 * B * (double)max_len * H_kv * D * 4, p.chunk_o,
-                   p.splits_o, p.tiles_o, p.ksplit_o, p.parts_o);
+                   p.kind_p != kKvNone, own, p.chunk_o, p.splits_o, p.tiles_o, p.ksplit_o,
+                   p.parts_o);
         // sum of ceil(n_b / block) over the sequences of more than `few` tokens
         const int block = (p.ksplit_o ? 1 : 2) * (128 / group), most = n_tokens / (few + 1);
         p.row_blocks_t = n_tokens / block + (B < most ? B : most);
         p.tiles_o = 1;
-        tiles_b = some;
+        tiles_b = few > 0 ? some : 0;
         groups += tiles_b * ceil_div(max_len, group_keys(D)) * H_kv;
     }
     p.direct = p.kind_p == kKvNone && p.parts_o == 1;
     p.blocks = (p.kind_p == kKvTiles ? (long long)p.splits_p * H_kv * p.tiles_p : 0) +
-               (p.kind_o == kKvTiles ? (long long)B * p.splits_o * H_kv * p.tiles_o : 0) +
+               (p.kind_o == kKvTiles && !packed ? (long long)B * p.splits_o * H_kv * p.tiles_o : 0) +
                (long long)p.row_blocks_t * p.splits_o * H_kv;
     long long bytes = p.direct ? 0 : (p.parts_p + p.parts_o) * part_bytes;
     if (groups > 0) {

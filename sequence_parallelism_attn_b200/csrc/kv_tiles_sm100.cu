@@ -58,7 +58,7 @@ struct __align__(64) TileParams {
     int chunk_p, splits_p, blocks_p, ksplit_p, part_p;  // prefix: keys per split, ...
     int chunk_o, splits_o, blocks_o, ksplit_o, part_o;  // own keys; first partial index
     unsigned items_p;
-    int few;         // > 0: the packed form
+    int few;         // the packed form: sequences of more tokens
     int direct;
     float scale_log2;
     float* parts;    // [part][token][head][D]
@@ -799,8 +799,9 @@ cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& plan, unsigned long l
     p.items_p = has_p ? (unsigned)((long long)plan.splits_p * a.H_kv * plan.tiles_p) : 0;
     const long long grid =
         p.items_p +
-        (plan.few ? (long long)plan.row_blocks_t
-                  : plan.kind_o == kKvTiles ? (long long)a.B * plan.tiles_o : 0) *
+        (plan.row_blocks_t         ? (long long)plan.row_blocks_t
+         : plan.kind_o == kKvTiles ? (long long)a.B * plan.tiles_o
+                                   : 0) *
             plan.splits_o * a.H_kv;
     p.few = plan.few;
     p.direct = plan.direct;
@@ -819,7 +820,7 @@ cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& plan, unsigned long l
         return cudaErrorInvalidValue;
     }
     const unsigned n = (unsigned)grid;
-    if (plan.few)
+    if (plan.row_blocks_t)
         return a.D == 128 ? launch<128, true>(p, n, why) : launch<64, true>(p, n, why);
     return a.D == 128 ? launch<128, false>(p, n, why) : launch<64, false>(p, n, why);
 }

@@ -114,6 +114,11 @@ PREFIX = [  # n, lens, page, hq, hkv, d, prefix
     ([1, 129, 1, 1], [200, 129, 3, 40], 8, 24, 1, 64, 19),
     ([1] * 40 + [66] + [1] * 40, [1 + 7 * i for i in range(40)] + [66] + [3] * 40, 16, 4, 4, 64, 0),
     ([0] * 33 + [90] + [1] * 1200, [0] * 33 + [90] + [1 + i % 9 for i in range(1200)], 16, 2, 1, 64, 3),
+    # the same with more than 32 heads per kv head: all of them behind many rows
+    ([1, 1, 0, 1, 40], [50, 300, 0, 1, 45], 16, 48, 1, 64, 0),
+    ([1] * 40 + [30] + [2] * 3, [1 + 7 * i for i in range(40)] + [66] + [3] * 3, 64, 64, 1, 128, 40),
+    ([0, 9, 1, 1], [5, 9, 1, 500], 8, 128, 1, 64, 0),
+    ([1, 1, 1, 17], [1500, 3, 0, 700], 128, 80, 2, 128, 0),
 ]
 
 

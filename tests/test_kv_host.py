@@ -110,6 +110,20 @@ def test_workspace_follows_the_tokens(lib):
     assert size(1 << 16, 10, 1, 4000, 0, 32, 8, 128, 16) <= size(1 << 4, 10, 1, 4000, 0, 32, 8, 128, 16)
 
 
+@pytest.mark.parametrize("kw", [
+    # single tokens and one prompt, tables for 131072 keys, pages that the tile kernel does not take
+    dict(B=256, N=2255, T=2000, hq=32, hkv=8, d=128, qs=4096, page=24, ps=24576, mp=5462,
+         max_len=131072),
+    # and one of a million tokens with 128 heads to a kv head
+    dict(B=4096, N=(1 << 20) + 4095, T=1 << 20, hq=128, hkv=1, qs=8192, ps=1024, mp=1 << 16),
+])
+def test_ragged_batches_are_not_too_large(lib, kw):
+    """What a launch would need follows the tokens: such a batch is refused for the workspace
+    that is missing here, not for its size."""
+    assert call(lib, "ra_prefix_attn_fwd", PREFIX, kw | dict(wsb=16)) == 1
+    assert b"workspace" in lib.ra_last_error()
+
+
 def test_binding_refusals():
     """The binding checks shapes, types and layouts before the library is called."""
     from sequence_parallelism_attn_b200 import ra
