@@ -565,7 +565,8 @@ RA_API ra_status ra_cross_attn_bwd(const void* q, const void* k, const void* v,
  * ra_sync_status -- synchronise `stream`, then read and clear this device's
  * kernel error word.  Returns RA_ERR_TIMEOUT if a kernel launched since the
  * last call gave up on a bounded wait, RA_ERR_INDEX if one met an index outside
- * its bounds, RA_ERR_CUDA if the synchronisation itself failed, RA_OK otherwise.
+ * its bounds (after both, RA_ERR_TIMEOUT first and RA_ERR_INDEX at the next call),
+ * RA_ERR_CUDA if the synchronisation itself failed, RA_OK otherwise.
  */
 RA_API ra_status ra_sync_status(void* stream);
 

@@ -108,7 +108,9 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& p, unsigned long long wait_
                       const char** why);
 cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& p, unsigned long long wait_limit_ns,
                             const char** why);
-cudaError_t read_and_clear_kv_tile_error(unsigned int* value);
+// The tile kernel's word: waits that ran out in bits 0 - 7, cache errors above them, which are
+// left as they are unless all is set.
+cudaError_t read_and_clear_kv_tile_error(unsigned int* value, bool all);
 cudaError_t read_and_clear_kv_cluster_error(unsigned int* value);
 
 struct CrossBwdArgs {

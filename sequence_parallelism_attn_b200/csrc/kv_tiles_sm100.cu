@@ -825,13 +825,12 @@ cudaError_t launch_kv_tiles(const KvArgs& a, const KvPlan& plan, unsigned long l
     return a.D == 128 ? launch<128, false>(p, n, why) : launch<64, false>(p, n, why);
 }
 
-cudaError_t read_and_clear_kv_tile_error(unsigned int* value) {
+cudaError_t read_and_clear_kv_tile_error(unsigned int* value, bool all) {
     cudaError_t e = cudaMemcpyFromSymbol(value, g_kv_tile_error_word, sizeof(unsigned int));
     if (e != cudaSuccess) return e;
-    if (*value) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_kv_tile_error_word, &zero, sizeof(unsigned int));
-    }
+    const unsigned int kept = all ? 0u : *value & ~255u;
+    if (*value != kept)
+        e = cudaMemcpyToSymbol(g_kv_tile_error_word, &kept, sizeof(unsigned int));
     return e;
 }
 

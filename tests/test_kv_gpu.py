@@ -400,6 +400,28 @@ def test_indices_out_of_bounds_are_reported(ra_lib):
     run(cu=i32([-5, 1, 2]).to(DEV))
 
 
+@pytest.mark.parametrize("n,lens", [([1, 1], [20, 30]), ([1, 1], [20, 20000]),
+                                    ([300, 1, 1], [320, 20, 20]), ([300, 300], [320, 320])])
+def test_a_bad_index_beside_a_wait_that_ran_out(ra_lib, n, lens):
+    """Both are reported, the wait first (the ring kernel's test hook withholds a load)."""
+    x = Batch(n, lens, 16, 1, 64, seed=6, fill=0.0)
+    q = randn(x.N, 1, 64, seed=2).to(DEV)
+    kp, vp, cu, lens_, tables = x.gpu("kp", "vp", "cu", "lens", "tables")
+    ring = [torch.zeros(s, dtype=torch.bfloat16, device=DEV) for s in
+            [(1, 256, 1, 64), (1, 1, 256, 1, 64), (1, 1, 256, 1, 64)]]
+    old = ra_lib.ra_set_wait_limit_ns(20_000_000)
+    try:
+        ra_lib.ra_debug_inject_stall(True)
+        ra_lib.ring_attn_fwd(*ring, False)
+        bad = tables.clone()
+        bad[0, 0] = x.n_pages
+        ra_lib.prefix_attn_fwd(q, kp, vp, cu, lens_, bad, max(n), max_len=max(lens))
+        status = [ra_lib.load().ra_sync_status(None) for _ in range(3)]
+    finally:
+        ra_lib.ra_set_wait_limit_ns(old)
+    assert status == [4, 5, 0]
+
+
 @pytest.mark.parametrize("lens,width", [([20, 30], 1), ([20, 30], 4000), ([80, 50], 1),
                                         ([80, 50, 9, 9], 1)])
 def test_token_rows_out_of_bounds_are_reported(ra_lib, lens, width):
