@@ -18,6 +18,7 @@ thread_local int g_inject_stall = 0;
 constexpr unsigned long long kDefaultWaitLimitNs = 4000000000ull;
 std::atomic<unsigned long long> g_wait_limit_ns{kDefaultWaitLimitNs};
 std::atomic<int> g_bwd_deterministic{0};
+std::atomic<bool> g_cache_kernels{false};
 
 ra_status fail(ra_status s, const std::string& msg) {
     g_last_error = msg;
@@ -39,6 +40,7 @@ namespace ra {
 int set_last_error(int status, const std::string& msg) { return (int)fail((ra_status)status, msg); }
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 int bwd_deterministic() { return g_bwd_deterministic.load(); }
+void cache_kernels_in_use() { g_cache_kernels.store(true, std::memory_order_relaxed); }
 }  // namespace ra
 
 extern "C" {
@@ -379,7 +381,8 @@ ra_status ra_sync_status(void* stream) {
     if (e == cudaSuccess) e = ra::read_and_clear_permute_error(&pword);
     if (e == cudaSuccess) e = ra::read_and_clear_bwd_error(&bword);
     unsigned int kword = 0, aword = 0, tword = 0, cword = 0;
-    if (e == cudaSuccess) e = ra::read_and_clear_kv_tile_error(&tword, false);
+    const bool cache = g_cache_kernels.load(std::memory_order_relaxed);
+    if (e == cudaSuccess && cache) e = ra::read_and_clear_kv_tile_error(&tword, false);
     if (e != cudaSuccess) return cuda_fail(e, "reading the kernel error word");
     word |= (pword ? 16u : 0u) | (bword ? 64u : 0u) | ((tword & 255u) ? 128u : 0u);
     if (word) {
@@ -389,6 +392,7 @@ ra_status ra_sync_status(void* stream) {
                       "4 softmax, 8 drain, 16 permute, 64 backward, 128 cache tiles)", word);
         return fail(RA_ERR_TIMEOUT, buf);
     }
+    if (!cache) return RA_OK;
     // (after a wait that ran out the words of bad indices stay for the next call)
     e = ra::read_and_clear_kv_error(&kword);
     if (e == cudaSuccess) e = ra::read_and_clear_kv_cluster_error(&cword);

@@ -13,6 +13,10 @@ constexpr int kSms = 148;  // a B200's SMs: the work split is planned for them, 
 // Bits of the device's cache error word (read and cleared by ra_sync_status).
 constexpr unsigned kKvErrTokens = 1u, kKvErrLength = 2u, kKvErrPage = 4u;
 
+// Called by every launch of the cache kernels (a captured one too): from the first on,
+// ra_sync_status reads their error words, at 13 us each.
+void cache_kernels_in_use();
+
 // Sequence b's token rows: the first, and their number, kept within the token tensors
 // whatever cu holds; bad where it was outside the call's bounds.
 struct TokenRows {

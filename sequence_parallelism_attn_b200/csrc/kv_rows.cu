@@ -781,6 +781,7 @@ KvPlan plan_kv(int B, int n_tokens, int max_tokens, int max_len, int prefix_len,
 
 cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wait_limit_ns,
                       const char** why) {
+    cache_kernels_in_use();
     cudaError_t e = cudaSuccess;
     const bool tiled = plan.kind_p == kKvTiles || plan.kind_o == kKvTiles || plan.few;
     if (tiled) {

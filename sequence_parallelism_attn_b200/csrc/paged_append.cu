@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(384) append_kernel(const __grid_constant__ App
 }  // namespace
 
 cudaError_t launch_paged_append(const AppendArgs& a) {
+    cache_kernels_in_use();
     AppendParams p;
     p.a = a;
     p.tiles = (a.max_tokens + kTokens - 1) / kTokens;
