@@ -542,7 +542,8 @@ RA_API ra_status ra_cross_attn_fwd(const void* q, const void* k, const void* v,
  * given dout (the formulas of ra_ring_attn_bwd over the keys j < kv_lens[b]; with grouped
  * heads dk and dv are the sums over the group).  Rows of dk and dv past kv_lens[b] are zero,
  * and so is dq of a batch row without keys.
- *   q, k, v, kv_lens, sizes, strides, scale   as given to ra_cross_attn_fwd.
+ *   q, k, v, kv_lens, sizes, strides, scale   as given to ra_cross_attn_fwd (kv_lens above Lk
+ *              is cut and reported likewise).
  *   out, dout  device bf16, dense [B][Lq][H_q][D]: the forward's output, and the gradient.
  *   lse        device fp32, [B][H_q][Lq]: the forward's.
  *   grad_dtype RA_FP32 or RA_BF16 (sums in fp32, rounded once): dq dense [B][Lq][H_q][D],

@@ -379,12 +379,12 @@ ra_status ra_sync_status(void* stream) {
     unsigned int word = 0, pword = 0, bword = 0;
     e = ra::read_and_clear_error_word(&word);
     if (e == cudaSuccess) e = ra::read_and_clear_permute_error(&pword);
-    if (e == cudaSuccess) e = ra::read_and_clear_bwd_error(&bword);
+    if (e == cudaSuccess) e = ra::read_and_clear_bwd_error(&bword, false);
     unsigned int kword = 0, aword = 0, tword = 0, cword = 0;
     const bool cache = g_cache_kernels.load(std::memory_order_relaxed);
     if (e == cudaSuccess && cache) e = ra::read_and_clear_kv_tile_error(&tword, false);
     if (e != cudaSuccess) return cuda_fail(e, "reading the kernel error word");
-    word |= (pword ? 16u : 0u) | (bword ? 64u : 0u) | ((tword & 255u) ? 128u : 0u);
+    word |= (pword ? 16u : 0u) | ((bword & 255u) ? 64u : 0u) | ((tword & 255u) ? 128u : 0u);
     if (word) {
         char buf[160];
         std::snprintf(buf, sizeof buf,
@@ -392,14 +392,14 @@ ra_status ra_sync_status(void* stream) {
                       "4 softmax, 8 drain, 16 permute, 64 backward, 128 cache tiles)", word);
         return fail(RA_ERR_TIMEOUT, buf);
     }
-    if (!cache) return RA_OK;
     // (after a wait that ran out the words of bad indices stay for the next call)
-    e = ra::read_and_clear_kv_error(&kword);
-    if (e == cudaSuccess) e = ra::read_and_clear_kv_cluster_error(&cword);
-    if (e == cudaSuccess) e = ra::read_and_clear_append_error(&aword);
+    if (bword) e = ra::read_and_clear_bwd_error(&bword, true);
+    if (e == cudaSuccess && cache) e = ra::read_and_clear_kv_error(&kword);
+    if (e == cudaSuccess && cache) e = ra::read_and_clear_kv_cluster_error(&cword);
+    if (e == cudaSuccess && cache) e = ra::read_and_clear_append_error(&aword);
     if (e == cudaSuccess && tword) e = ra::read_and_clear_kv_tile_error(&tword, true);
     if (e != cudaSuccess) return cuda_fail(e, "reading the kernel error word");
-    kword |= aword | cword | (tword >> 8);
+    kword |= aword | cword | (tword >> 8) | (bword >> 8);
     if (kword) {
         char buf[160];
         std::snprintf(buf, sizeof buf,

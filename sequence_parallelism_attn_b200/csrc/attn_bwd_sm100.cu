@@ -25,12 +25,13 @@
 #include <cstdint>
 #include "ra_internal.h"
 #include "attn_sched.cuh"
+#include "kv_internal.h"
 #include "sm100_ptx.cuh"
 #include "../../include/ra.h"
 
 namespace ra {
 
-__device__ unsigned int g_bwd_error_word = 0;
+__device__ unsigned int g_bwd_error_word = 0;  // waits: bits 0-4; cross attention's lengths: << 8
 
 namespace {
 
@@ -912,6 +913,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_sm100(const __grid_constant__
         mbar_init(bar(C::BAR_ACC), 2);    // dV from A, dK from B
         mbar_init(bar(C::BAR_DRAIN), 3);  // A, B, C
         if (CROSS) mbar_init(land, 1);
+        if (CROSS && kt == 0 && g == 0 && p.kv_lens && p.kv_lens[b] > p.Lc)
+            atomicOr(&g_bwd_error_word, kKvErrLength << 8);
         *abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -1622,13 +1625,11 @@ cudaError_t launch_attn_bwd_sm100(const AttnBwdArgs& a, unsigned long long wait_
     return cudaErrorInvalidValue;
 }
 
-cudaError_t read_and_clear_bwd_error(unsigned int* value) {
+cudaError_t read_and_clear_bwd_error(unsigned int* value, bool all) {
     cudaError_t e = cudaMemcpyFromSymbol(value, g_bwd_error_word, sizeof(unsigned int));
     if (e != cudaSuccess) return e;
-    if (*value) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_bwd_error_word, &zero, sizeof(unsigned int));
-    }
+    const unsigned int kept = all ? 0u : *value & ~255u;
+    if (*value != kept) e = cudaMemcpyToSymbol(g_bwd_error_word, &kept, sizeof(unsigned int));
     return e;
 }
 

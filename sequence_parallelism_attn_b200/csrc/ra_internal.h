@@ -216,7 +216,9 @@ cudaError_t launch_ulysses_scatter(int mode, const void* in, void* const* dst, i
 // Tensor-core backward for bf16 inputs, D in {64, 128}: Delta, dQ, then dK/dV.
 cudaError_t launch_attn_bwd_sm100(const AttnBwdArgs& a, unsigned long long wait_limit_ns,
                                   const char** why);
-cudaError_t read_and_clear_bwd_error(unsigned int* value);
+// Waits that ran out in bits 0 - 7, cross attention's lengths out of bounds above them, which
+// are left as they are unless all is set.
+cudaError_t read_and_clear_bwd_error(unsigned int* value, bool all);
 
 // The process-wide settings of ra_set_wait_limit_ns and ra_set_bwd_deterministic.
 unsigned long long wait_limit_ns();

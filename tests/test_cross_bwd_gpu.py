@@ -69,6 +69,29 @@ def test_gradients_deterministic(ra_lib, deterministic, case):
     assert all(torch.equal(a, b) for a, b in zip(g, again))
 
 
+@pytest.mark.parametrize("mode", [False, True])
+@pytest.mark.parametrize("at", [0, 2])
+def test_key_counts_out_of_bounds(ra_lib, mode, at):
+    """A key count past the states is cut to them and reported, as by the forward; a negative one
+    is none."""
+    q, kv, do, lens = inputs(2, 17)
+    kv = kv.nan_to_num(0)
+    dev, lens = kv.to(DEV), list(lens)
+    lens[at], lens[1] = 78, -2
+    full = [77 if n > 77 else max(n, 0) for n in lens]
+    o, l = ra_lib.cross_attn_fwd(q.to(DEV), dev[:, :, 0], dev[:, :, 1], i32(full).to(DEV),
+                                 out_dtype=torch.bfloat16)
+    assert ra_lib.ra_sync_status() == 0
+    ra_lib.ra_set_bwd_deterministic(mode)
+    try:
+        g = ra_lib.cross_attn_bwd(q.to(DEV), dev[:, :, 0], dev[:, :, 1], o, l, do.to(DEV),
+                                  i32(lens).to(DEV))
+    finally:
+        ra_lib.ra_set_bwd_deterministic(False)
+    assert ra_lib.ra_sync_status() == 5 and ra_lib.ra_sync_status() == 0
+    ref.check_grads(g, ref.cross_backward(q, kv[:, :, 0], kv[:, :, 1], full, do, 0.125), "cut")
+
+
 def test_against_differences(ra_lib):
     """The gradients' inner product with a direction against the 64-bit loss's central
     difference along it (step 1e-5: its own error is about 1e-10 of the loss)."""
