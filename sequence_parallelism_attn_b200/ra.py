@@ -12,6 +12,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -446,6 +447,7 @@ def ring_attn_fwd(q: torch.Tensor, k_chunks, v_chunks, causal: bool, scale: floa
 
 # ------------------------------------------------------------------ attention over a K/V cache
 _native = None
+_native_lock = threading.Lock()
 
 
 def native():
@@ -454,17 +456,23 @@ def native():
     allocations run in C++."""
     global _native
     if _native is None:
-        load()
-        if not os.path.exists(NATIVE_PATH):
-            raise RuntimeError(f"{NATIVE_PATH} is missing: build it with "
-                               "`python -m sequence_parallelism_attn_b200.build` (no fallback path)")
-        loader = importlib.machinery.ExtensionFileLoader("_ra_torch", NATIVE_PATH)
-        spec = importlib.util.spec_from_loader("_ra_torch", loader)
-        module = importlib.util.module_from_spec(spec)
-        loader.exec_module(module)
-        module.set_error_class(RaError)
-        _native = module
+        with _native_lock:
+            if _native is None:
+                _native = _load_native()
     return _native
+
+
+def _load_native():
+    load()
+    if not os.path.exists(NATIVE_PATH):
+        raise RuntimeError(f"{NATIVE_PATH} is missing: build it with "
+                           "`python -m sequence_parallelism_attn_b200.build` (no fallback path)")
+    loader = importlib.machinery.ExtensionFileLoader("_ra_torch", NATIVE_PATH)
+    spec = importlib.util.spec_from_loader("_ra_torch", loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    module.set_error_class(RaError)
+    return module
 
 
 def _on(stream, t: torch.Tensor):

@@ -124,6 +124,42 @@ def test_ragged_batches_are_not_too_large(lib, kw):
     assert b"workspace" in lib.ra_last_error()
 
 
+def test_native_module_is_loaded_once(monkeypatch):
+    """Threads that ask for the native module at the same time get the same one, complete."""
+    import threading
+    import time
+
+    from sequence_parallelism_attn_b200 import build, ra
+    build.build()
+    made = []
+
+    class Loader:
+        def __init__(self, name, path):
+            pass
+
+        def create_module(self, spec):
+            made.append(type("Module", (), {})())
+            return made[-1]
+
+        def exec_module(self, module):
+            time.sleep(0.05)
+            module.set_error_class = lambda cls: setattr(module, "cls", cls)
+
+    monkeypatch.setattr(ra, "_native", None)
+    monkeypatch.setattr(ra.importlib.machinery, "ExtensionFileLoader", Loader)
+    got, start = [], threading.Barrier(8)
+
+    def ask():
+        start.wait()
+        m = ra.native()
+        got.append((m, getattr(m, "cls", None)))
+
+    threads = [threading.Thread(target=ask) for _ in range(8)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len(made) == 1 and got == [(made[0], ra.RaError)] * 8
+
+
 def test_binding_refusals():
     """The binding checks shapes, types and layouts before the library is called."""
     from sequence_parallelism_attn_b200 import ra
