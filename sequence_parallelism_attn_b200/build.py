@@ -22,9 +22,9 @@ LIB = os.path.join(HERE, "libra_b200.so")
 NATIVE = os.path.join(HERE, "_ra_torch.so")
 BINDING = "binding.cpp"
 BUILD_DIR = os.path.join(HERE, "_build")
-SOURCES = ["api.cu", "attn_sm100.cu", "attn_bwd_sm100.cu", "bwd_static.cu", "attn_fp32.cu", "lse_merge.cu", "permute.cu",
-           "api_kv.cu", "paged_append.cu", "kv_rows.cu", "cross_bwd.cu",
-           "kv_tiles_sm100.cu", "kv_cluster.cu"]
+SOURCES = ["api.cu", "attn_sm100.cu", "attn_bwd_sm100.cu", "bwd_static.cu", "attn_fp32.cu",
+           "lse_merge.cu", "permute.cu", "api_kv.cu", "paged_append.cu", "kv_rows.cu",
+           "cross_bwd.cu", "kv_tiles_sm100.cu", "kv_cluster.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
               "-fvisibility=hidden", f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -55,13 +55,18 @@ def _run(cmd, verbose: bool) -> None:
 def build_native(force: bool = False, verbose: bool = False) -> str:
     """The native Python module over the library (csrc/binding.cpp), linked to it by a path
     relative to itself."""
-    src = os.path.join(CSRC, BINDING)
-    if not force and os.path.exists(NATIVE) and \
-            os.path.getmtime(NATIVE) >= _mtime(src, os.path.join(INCLUDE, "ra.h")):
-        return NATIVE
     import sysconfig
 
     import torch
+    src = os.path.join(CSRC, BINDING)
+    # it holds torch's and Python's ABI, so it is out of date too when one of them has changed
+    stamp = os.path.join(BUILD_DIR, "native.stamp")
+    built_for = f"torch {torch.__version__}, Python {sys.version}"
+    if not force and os.path.exists(NATIVE) and os.path.exists(stamp) and \
+            os.path.getmtime(NATIVE) >= _mtime(src, os.path.join(INCLUDE, "ra.h")):
+        with open(stamp) as f:
+            if f.read() == built_for:
+                return NATIVE
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = NATIVE + ".tmp"
@@ -71,6 +76,9 @@ def build_native(force: bool = False, verbose: bool = False) -> str:
           "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", f"-L{HERE}",
           f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(tmp, NATIVE)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return NATIVE
 
 

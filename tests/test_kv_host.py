@@ -124,6 +124,28 @@ def test_ragged_batches_are_not_too_large(lib, kw):
     assert b"workspace" in lib.ra_last_error()
 
 
+def test_native_module_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
+    from sequence_parallelism_attn_b200 import build
+    runs = []
+
+    def compile_(cmd, verbose):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(build, "_run", compile_)
+    monkeypatch.setattr(build, "NATIVE", str(tmp_path / "_ra_torch.so"))
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path / "_build"))
+    for want in (1, 1):
+        build.build_native()
+        assert len(runs) == want
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    for want in (2, 2):
+        build.build_native()
+        assert len(runs) == want
+    build.build_native(force=True)
+    assert len(runs) == 3
+
+
 def test_native_module_is_loaded_once(monkeypatch):
     """Threads that ask for the native module at the same time get the same one, complete."""
     import threading
