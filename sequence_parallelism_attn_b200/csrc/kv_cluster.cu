@@ -1,9 +1,9 @@
 // kv_cluster.cu -- attention of few query rows over a moderate number of keys, where the time
 // of a call is latency: one kernel, without partial results in memory.
 //
-// A cluster of up to eight blocks takes one (sequence, kv head, row tile).  Its warps share
-// out the groups of the prefix's keys and of the sequence's own, each warp with a ring and a
-// softmax state as in kv_rows.cu; a block merges its four states in shared memory, the
+// A cluster of up to eight blocks takes one (sequence, kv head), whose rows (32 at most) are
+// one row tile.  Its warps share out the groups of the prefix's keys and of the sequence's own,
+// each warp with a ring and a softmax state as in kv_rows.cu; a block merges its four states in shared memory, the
 // cluster's blocks read one another's merged states through distributed shared memory, each
 // for its part of the rows, and write the result.  Every sequence reads the prefix for itself
 // (from L2 after the first): with few sequences, or a short prefix, that costs less than the
@@ -66,14 +66,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     const KvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank(), n_ranks = (int)cluster_size();
-    int j = (int)(blockIdx.x / (unsigned)n_ranks);
-    const int tile = j % p.p.tiles_o;
-    j /= p.p.tiles_o;
-    const int g = j % a.H_kv;
+    const int j = (int)(blockIdx.x / (unsigned)n_ranks), g = j % a.H_kv;
 
     Seq s;
     s.b = j / a.H_kv;
-    const bool reports = rank == 0 && threadIdx.x == 0 && g == 0 && tile == 0;
+    const bool reports = rank == 0 && threadIdx.x == 0 && g == 0;
     if (a.cu) {
         const TokenRows rows = token_rows(a.cu, s.b, a.n_tokens, a.max_tokens);
         if (rows.bad && reports) atomicOr(&g_kv_cluster_error_word, kKvErrTokens);
@@ -83,7 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         s.tok0 = s.b * a.max_tokens;
         s.n_tok = a.max_tokens;
     }
-    if (tile * R >= s.n_tok * p.group) return;  // the same for the whole cluster
+    if (s.n_tok == 0) return;  // the same for the whole cluster
     s.len = a.lens ? max(a.lens[s.b], 0) : a.max_len;
     if (s.len > a.max_len) {
         if (reports) atomicOr(&g_kv_cluster_error_word, kKvErrLength);
@@ -168,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     bool own = false;
     for (int i = 1 - C::STAGES; i < max(cnt, 1); ++i) {
         if (i == 0) {  // the rows' Q, behind the first loads
-            r.start(p, s, g, tile, a.causal);
+            r.start(p, s, g, 0, a.causal);
             own_min = r.min_limit;
             r.min_limit = a.prefix_len;
 #pragma unroll
@@ -227,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     constexpr int TPR = D / 4, RPP = kWarps * 32 / TPR;  // threads per row, rows per pass
     const int c4 = threadIdx.x % TPR;
     // (where no state has a finite maximum the sums are 0, or a NaN that has to come through)
-    const int rows = min(s.n_tok * p.group - tile * R, R);
+    const int rows = s.n_tok * p.group;  // <= R
     for (int row = threadIdx.x / TPR; row < rows; row += RPP) {
         float mm = -INFINITY;
 #pragma unroll
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
             acc.w = fmaf(f, v.w, acc.w);
         }
         const float inv = lu == 0.f ? 0.f : 1.f / lu;
-        const int at = tile * R + row, t = fdiv(at, p.dgroup), head = g * p.group + at - t * p.group;
+        const int t = fdiv(row, p.dgroup), head = g * p.group + row - t * p.group;
         const long long orow = (long long)(s.tok0 + t) * a.H_q + head;
         if (a.out_bf16)
             *reinterpret_cast<uint2*>((uint16_t*)a.out + orow * D + c4 * 4) =

@@ -55,7 +55,6 @@ __device__ __forceinline__ Seq get_seq(const RowsParams& p, int b) {
             s.n_tok = a.max_tokens;
         }
         s.len = a.lens ? min(max(a.lens[b], 0), a.max_len) : a.max_len;
-        if (p.p.kind_o == kKvTiles) s.len = 0;
         s.table = a.tables ? a.tables + (long long)b * a.max_pages : nullptr;
     }
     s.groups = (s.len + KEYS - 1) / KEYS;
@@ -619,7 +618,6 @@ bool plan_cluster(int B, long long rows, bool tiles_p, int max_len, int prefix_l
     p = KvPlan{};
     p.kind_o = kKvCluster;
     p.mt = rows > 16 ? 2 : 1;
-    p.tiles_o = 1;
     p.cluster = c;
     p.direct = 1;
     p.blocks = js * c;
