@@ -435,6 +435,7 @@ RA_API ra_status ra_ulysses_head2seq_grouped(const void* in, void* out, int P, i
  *     included (they are the last n_b of them).
  *   - block_tables: device int32, [B][max_pages]: key j of sequence b is row j % page_size of
  *     page block_tables[b][j / page_size].  Entries past a sequence's length are not read.
+ *   - n_tokens <= 2^24, B <= 2^28, max_len and prefix_len <= 2^30 (RA_ERR_INVALID above).
  *   - The device arrays may change between launches of a captured graph; host arguments are
  *     bounds and stay.  The first call of a kind in a process loads its kernels: make it
  *     before a capture.

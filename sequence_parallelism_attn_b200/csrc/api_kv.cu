@@ -21,7 +21,7 @@ bool aligned(const void* p, unsigned n) {
 }
 
 // Tokens and heads of a call fit the 32-bit indices of the kernels.
-constexpr long long kMaxTokens = 1ll << 24, kMaxKeys = 1ll << 30;
+constexpr long long kMaxTokens = 1ll << 24, kMaxKeys = 1ll << 30, kMaxSequences = 1ll << 28;
 
 ra_status check_heads(int H_q, int H_kv, int D, ra_dtype dtype) {
     if (H_kv < 1 || H_q < 1 || D < 1) return fail(RA_ERR_INVALID, "H_q, H_kv and D must be >= 1");
@@ -43,8 +43,9 @@ ra_status check_batch(const int* cu, const int* lens, const int* tables, int B, 
                       int max_tokens) {
     if (B < 1 || n_tokens < 1 || max_tokens < 1)
         return fail(RA_ERR_INVALID, "B, n_tokens and max_tokens must be >= 1");
-    if (n_tokens > kMaxTokens || max_tokens > n_tokens)
-        return fail(RA_ERR_INVALID, "n_tokens must be <= 2^24 and max_tokens <= n_tokens");
+    if (n_tokens > kMaxTokens || max_tokens > n_tokens || B > kMaxSequences)
+        return fail(RA_ERR_INVALID,
+                    "n_tokens must be <= 2^24, max_tokens <= n_tokens and B <= 2^28");
     if (!aligned(cu, 4) || !aligned(lens, 4) || !aligned(tables, 4))
         return fail(RA_ERR_INVALID,
                     "cu_tokens, seq_lens and block_tables must be non-null and 4-byte aligned");
@@ -115,8 +116,6 @@ ra_status ra_paged_kv_append(const void* q, const void* k, const void* v, long l
     if (interleaved != 0 && interleaved != 1)
         return fail(RA_ERR_INVALID, "interleaved must be 0 or 1");
     if (pos_offset < 0) return fail(RA_ERR_INVALID, "pos_offset must be >= 0");
-    if ((long long)B * max_tokens > 0x7fffffffLL)
-        return fail(RA_ERR_INVALID, "B * max_tokens must be below 2^31");
     ra::AppendArgs a;
     a.q = q;
     a.k = k;

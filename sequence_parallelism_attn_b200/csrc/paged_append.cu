@@ -198,7 +198,6 @@ cudaError_t launch_paged_append(const AppendArgs& a) {
     p.tiles = (a.max_tokens + kTokens - 1) / kTokens;
     const int units = (a.H_q + 2 * a.H_kv) * (a.D / 16);
     const int threads = units >= 384 ? 384 : ((units + 31) / 32) * 32;
-    unsigned grid = (unsigned)((long long)p.tiles * a.B);
     // Flat where at least half of the blocks by sequence would be empty.  Measured, us on the GPU,
     // by sequence and flat (32 + 2 x 8 heads of 128): 16 and 1 tokens in turn, 128 sequences, 8.2,
     // 7.0; 1000 and 500, 8 sequences, 27.7, 33.1 (the look-up comes before a block's stores); 255
@@ -206,11 +205,12 @@ cudaError_t launch_paged_append(const AppendArgs& a) {
     const long long flat = (a.n_tokens + kTokens - 1) / kTokens;
     if ((long long)p.tiles * a.B >= 2 * (flat + a.B)) {
         p.tiles = 0;
-        grid = (unsigned)flat;
-        if (a.D == 128) append_kernel<128, true><<<grid, threads, 0, a.stream>>>(p);
-        else append_kernel<64, true><<<grid, threads, 0, a.stream>>>(p);
+        const unsigned rows = (unsigned)flat;
+        if (a.D == 128) append_kernel<128, true><<<rows, threads, 0, a.stream>>>(p);
+        else append_kernel<64, true><<<rows, threads, 0, a.stream>>>(p);
         return cudaGetLastError();
     }
+    const unsigned grid = (unsigned)((long long)p.tiles * a.B);  // < 2 (2^22 + 2^28)
     if (a.D == 128) append_kernel<128, false><<<grid, threads, 0, a.stream>>>(p);
     else append_kernel<64, false><<<grid, threads, 0, a.stream>>>(p);
     return cudaGetLastError();

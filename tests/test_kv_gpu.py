@@ -529,6 +529,29 @@ def test_append(ra_lib, case):
         assert got is None
 
 
+def test_append_of_a_very_long_run(ra_lib):
+    """One run of 2^20 tokens among 4095 single ones: more than 2^31 places by sequence."""
+    page, B, run = 256, 4096, 1 << 20
+    lens = torch.ones(B, dtype=torch.int32)
+    lens[7] = run
+    cu = torch.cat([i32([0]), lens.cumsum(0).int()])
+    N, pages = int(cu[-1]), B - 1 + run // page
+    ids = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).int()
+    tables = torch.full((B, run // page), 1 << 29, dtype=torch.int32)
+    tables[7] = ids[B - 1:]
+    tables[torch.arange(B) != 7, 0] = ids[:B - 1]
+    k, v = randn(N, 1, 64, seed=1).to(DEV), randn(N, 1, 64, seed=2).to(DEV)
+    kp, vp = torch.zeros(2, pages, page, 1, 64, dtype=torch.bfloat16, device=DEV)
+    ra_lib.paged_kv_append(None, k, v, kp, vp, cu.to(DEV), lens.to(DEV), tables.to(DEV), None, run)
+    assert ra_lib.ra_sync_status() == 0
+    ids = ids.long().to(DEV)
+    single = torch.cat([torch.arange(7), torch.arange(7 + run, N)]).to(DEV)
+    for pool, x in ((kp, k), (vp, v)):
+        assert torch.equal(pool[ids[B - 1:]].view(run, 1, 64), x[7:7 + run])
+        assert torch.equal(pool[ids[:B - 1], 0], x[single])
+        assert not pool[ids[:B - 1], 1:].any()
+
+
 def test_append_in_place_query(ra_lib):
     x = Batch([3, 2], [9, 2], 16, 2, 64, seed=8)
     q, k, v = (randn(5, h, 64, seed=h).to(DEV) for h in (4, 2, 2))

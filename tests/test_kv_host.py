@@ -41,7 +41,7 @@ def call(lib, entry, base, kw):
     (dict(hq=3), 1), (dict(hkv=0), 1), (dict(rot=8), 1), (dict(rot=80), 1), (dict(rot=-16), 1),
     (dict(inter=2), 1), (dict(off=-1), 1), (dict(page=0), 1), (dict(n=0), 1), (dict(mp=0), 1),
     (dict(ps=2040), 1), (dict(ps=2049), 1), (dict(d=96), 2), (dict(dt=1), 2), (dict(dt=7), 1),
-    (dict(N=1 << 25), 1), (dict(qo=FAKE, qos=512), 1),
+    (dict(N=1 << 25), 1), (dict(qo=FAKE, qos=512), 1), (dict(B=(1 << 28) + 1), 1),
 ])
 def test_append_refusals(lib, kw, status):
     assert call(lib, "ra_paged_kv_append", APPEND, kw) == status
