@@ -429,8 +429,9 @@ RA_API ra_status ra_ulysses_head2seq_grouped(const void* in, void* out, int P, i
  *     rows cu_tokens[b] .. cu_tokens[b+1]-1 of q, k, v and out (cu_tokens: device int32,
  *     [B+1], not decreasing, starting at >= 0).  Rows at or past cu_tokens[B] (a padded
  *     batch) and rows before cu_tokens[0] (a slice of a batch, given with all its token
- *     rows) take no part: nothing depends on them and they are not written.  n_tokens: rows of the token tensors, the host's
- *     bound on cu_tokens[B]; max_tokens: the host's bound on every n_b.
+ *     rows) take no part: nothing depends on them and they are not written.  n_tokens: rows
+ *     of the token tensors, the host's bound on cu_tokens[B]; max_tokens: the host's bound on
+ *     every n_b.
  *   - seq_lens: device int32, [B]: keys of sequence b's own in the cache, its new tokens
  *     included (they are the last n_b of them).
  *   - block_tables: device int32, [B][max_pages]: key j of sequence b is row j % page_size of
@@ -440,9 +441,9 @@ RA_API ra_status ra_ulysses_head2seq_grouped(const void* in, void* out, int P, i
  *     bounds and stay.  The first call of a kind in a process loads its kernels: make it
  *     before a capture.
  *   - Device values outside their bounds (cu_tokens below 0, decreasing or above n_tokens,
- *     n_b > max_tokens, seq_lens[b] > max_len or < n_b for the append, a page id outside [0, n_pages)) are never followed: the kernel skips
- *     or clamps them, what it writes for that sequence is undefined, and ra_sync_status()
- *     returns RA_ERR_INDEX.
+ *     n_b > max_tokens, seq_lens[b] > max_len or < n_b for the append, a page id outside
+ *     [0, n_pages)) are never followed: the kernel skips or clamps them, what it writes for
+ *     that sequence is undefined, and ra_sync_status() returns RA_ERR_INDEX.
  */
 
 /*
@@ -482,8 +483,10 @@ RA_API ra_status ra_paged_kv_append(const void* q, const void* k, const void* v,
  * sequences share a prefix (a system prompt, a document) kept once in the cache.
  * Token i of sequence b's n_b sees the prefix_len keys of the prefix and its own keys
  * 0 .. seq_lens[b] - n_b + i; out and lse are ra_ring_attn_fwd's formulas over those keys.
- * The prefix's keys are read once for the rows of the whole batch, each sequence's own keys
- * once for its rows; the parts are joined by the log-sum-exp merge of ra_lse_merge.
+ * The prefix is attended by the rows of the whole batch together, its keys read once for a
+ * tile of them (up to 256 rows, tokens x query heads of a kv head; small calls read it once
+ * for each sequence, from L2 after the first), each sequence's own keys once for a tile of its
+ * rows; the parts are joined by the log-sum-exp merge of ra_lse_merge.
  * prefix_len = 0 is plain paged attention (one token per sequence: decode).  A row that sees
  * no key gets out = 0, lse = -inf.  Keys and values that no row may see (past seq_lens[b],
  * past prefix_len) may hold anything, NaN included; a key that a later token of the same

@@ -9,6 +9,8 @@
 // (from L2 after the first): with few sequences, or a short prefix, that costs less than the
 // 5 us of a second kernel and the scan of the batch that kv_rows.cu needs.  4 sequences of 33
 // .. 300 keys behind 1000 (2 kv heads of 64) take 6.2 us, by kv_rows.cu and its combine 9.6.
+// With 17 to 32 rows of D = 128 the state and Q need more than the 255 registers: 52 to 80 bytes
+// are spilled.
 #include "kv_rows.cuh"
 
 namespace ra {

@@ -83,9 +83,9 @@ struct KvArgs {
 };
 
 // How a call is split.  The prefix and the sequences' own keys are each taken by one of two
-// kernels, or both by a third (kKvCluster): the tile kernel in ranges of `chunk` keys, each a partial result of its rows (two
-// where its warpgroups share a row tile), or the rows kernel, whose warps share the keys out
-// evenly among themselves.  The combine kernel joins the partials.
+// kernels, or both by a third (kKvCluster): the tile kernel in ranges of `chunk` keys, each a
+// partial result of its rows (two where its warpgroups share a row tile), or the rows kernel,
+// whose warps share the keys out evenly among themselves.  The combine kernel joins the partials.
 // kKvMixed (own keys): a ragged batch of long and short runs of new tokens, the rows kernel
 // for sequences of up to `few` tokens, the tile kernel for the others.
 constexpr int kKvNone = 0, kKvRows = 1, kKvTiles = 2, kKvCluster = 3, kKvMixed = 4;

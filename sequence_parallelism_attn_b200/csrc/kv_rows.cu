@@ -21,7 +21,9 @@
 // notes where and how many.
 //
 // What bounds it: 16 rows need 4 D flops per key against 4 D bytes of K and V, far below the
-// machine's balance, so it runs at the rate at which K and V arrive (6.2 TB/s over 786 MB).
+// machine's balance, so it runs at the rate at which K and V arrive (6.2 TB/s over 786 MB).  The
+// keys of the prefix are read once for each tile of 16 or 32 of the batch's rows.  A tile of 32
+// rows of D = 128 needs more than the 255 registers: 114 to 142 bytes are spilled.
 // Hence mma.sync on 16-row fragments (a tcgen05 tile has at least 64 rows) and the deep
 // per-warp rings.
 #include <cmath>
@@ -83,7 +85,8 @@ __device__ __forceinline__ void next_piece(const RowsParams& p, Place& x) {
 // PAGE16: a page holds whole runs of 16 keys (or the keys are dense); else every key is looked
 // up by itself.
 template <int D, int MT, bool PAGE16>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
+    kv_rows_kernel(const __grid_constant__ RowsParams p) {
     using C = RCfg<D, MT>;
     constexpr int R = C::ROWS, kKeys = C::KEYS, H16 = kKeys / 16;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -532,7 +535,8 @@ auto pick_combine(const KvPlan& p) {
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // The tile kernel's share of a plan over `units` (batch rows) x H_kv heads, `tokens` tokens
-// (`all_tokens` in all where the units differ, else 0) and `keys` keys each: row blocks, and the length of a key range, by a plain model.
+// (`all_tokens` in all where the units differ, else 0) and `keys` keys each: row blocks, and the
+// length of a key range, by a plain model.
 //   - A block costs its key tiles and three more for filling and draining, at tile_us each.
 //   - A row block's keys are cut into ranges of `per` tiles and a shorter last one; the full
 //     ranges come first in the grid, so the short ones fill up the SMs that a last wave of
@@ -632,13 +636,17 @@ KvPlan make_plan(int B, int n_tokens, int max_tokens, int max_len, int prefix_le
     // the tile kernel takes whole groups of heads, and pages that divide its 128-key tiles
     const bool tiles_ok =
         group <= 128 && (!paged || (page_size >= 8 && (page_size & (page_size - 1)) == 0));
-    // The most rows to leave to mma.sync: 32, but over many keys at D = 128 only 16, where a
-    // second fragment makes products and softmax the bound.  Measured, us, 8 tokens of 4 heads to
-    // a kv head (8 of 128), rows kernel or clusters against the tile kernel:
-    //   1 sequence: 2000 keys 13.8, 13.6    8000 keys 23.7, 17.1
-    //   8:  300 keys 14.2, 11.5    2000 keys 24.3, 17.7    8000 keys 77.7, 48.6
-    //   32: 300 keys 20.6, 25.3    2000 keys 84.1, 60.2    8000 keys 234, 199
-    // and 4 sequences of 8 rows behind a prefix: 8000 keys 25.0, 18.8    64000 keys 75.5, 55.0.
+    // The most rows to leave to mma.sync: 32, but over many keys at D = 128 only 16, where the
+    // second fragment's products, softmax and spilled registers (some 130 bytes a thread) are the
+    // bound.  Measured, us on the GPU, 8 tokens of 4 heads to a kv head (8 of 128), rows kernel or
+    // clusters against the tile kernel:
+    //   keys           300         600         1024        1500        2000
+    //   1 sequence     10.4, 12.4  12.4, 12.5  12.5, 12.5  14.5, 14.5  16.4, 16.6
+    //   8 sequences    16.5, 14.5  16.6, 15.3  18.6, 16.6  22.7, 18.6  26.8, 20.7
+    //   32 sequences   22.7, 28.9  31.7, 35.0  60.1, 43.5  74.5, 55.4  88.5, 65.6
+    // (8000 keys, calls: 23.7, 17.1;  77.7, 48.6;  234, 199) and 4 sequences of 8 rows behind a
+    // prefix: 8000 keys 25.0, 18.8    64000 keys 75.5, 55.0.  Below 1024 keys neither is the
+    // better for all batches: the rule goes by the keys alone, and 8 sequences of 300 lose 2 us.
     // At D = 64 (4 tokens of 8 heads to a kv head, 4 of them) 32 sequences over 8000 keys 63, 87.
     auto most_rows = [&](int keys) { return tiles_ok && D == 128 && keys >= 1024 ? 16 : 32; };
     const bool many = rows_o > most_rows(max_len);
@@ -812,14 +820,18 @@ cudaError_t launch_kv(const KvArgs& a, const KvPlan& plan, unsigned long long wa
         const bool page16 = !a.tables || a.page_size % 16 == 0;
         if (a.D == 128) {
             if (plan.mt == 1)
-                e = page16 ? launch_rows<128, 1, true>(p, grid, tiled) : launch_rows<128, 1, false>(p, grid, tiled);
+                e = page16 ? launch_rows<128, 1, true>(p, grid, tiled)
+                           : launch_rows<128, 1, false>(p, grid, tiled);
             else
-                e = page16 ? launch_rows<128, 2, true>(p, grid, tiled) : launch_rows<128, 2, false>(p, grid, tiled);
+                e = page16 ? launch_rows<128, 2, true>(p, grid, tiled)
+                           : launch_rows<128, 2, false>(p, grid, tiled);
         } else {
             if (plan.mt == 1)
-                e = page16 ? launch_rows<64, 1, true>(p, grid, tiled) : launch_rows<64, 1, false>(p, grid, tiled);
+                e = page16 ? launch_rows<64, 1, true>(p, grid, tiled)
+                           : launch_rows<64, 1, false>(p, grid, tiled);
             else
-                e = page16 ? launch_rows<64, 2, true>(p, grid, tiled) : launch_rows<64, 2, false>(p, grid, tiled);
+                e = page16 ? launch_rows<64, 2, true>(p, grid, tiled)
+                           : launch_rows<64, 2, false>(p, grid, tiled);
         }
     }
     if (e != cudaSuccess || (plan.direct && !plan.few)) return e;

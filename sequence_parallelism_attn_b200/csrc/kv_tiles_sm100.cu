@@ -21,8 +21,8 @@
 // us at D = 128 and 1.93 us at D = 64, where one row to a thread leaves the softmax's latency
 // in sight (MUFU 34%, issue slots 29% busy); a block costs some 6 us beside its key tiles.
 // Below 128 rows the rate at which K and V arrive.  1000 tokens of 32 heads behind 16384 keys
-// of 8 heads of 128: 310 us, 870 TFLOP/s, at the power cap.  Of 168 registers at launch, 60
-// bytes at most are spilled (make_item's; the packed form's search most of all).
+// of 8 heads of 128: 310 us, 870 TFLOP/s, at the power cap.  Up to 60 bytes a thread are
+// spilled (16 to 60 by instance).  The prefix's keys are read once for each row block.
 //
 // Every wait is bounded, as in attn_sm100.cu.
 #include <cuda.h>

@@ -3,8 +3,8 @@
 Argument marshalling only: torch tensors are turned into device pointers, sizes and
 the current CUDA stream; every step of the computation runs in the library's CUDA
 kernels.  The operators that run once per decoded token are marshalled by a native module
-(csrc/binding.cpp) over the same C ABI.  Loading fails loudly if the library has not been built -- there is no
-fallback path.
+(csrc/binding.cpp) over the same C ABI.  Loading fails loudly if the library has not been
+built -- there is no fallback path.
 """
 from __future__ import annotations
 
@@ -367,7 +367,8 @@ def ra_ulysses_head2seq_scatter(y: torch.Tensor, dst_ptrs, rank: int, stream=Non
 
 
 def ra_sync_status(stream=None) -> int:
-    """Synchronise the stream and return the kernel status (RA_OK or RA_ERR_TIMEOUT)."""
+    """Synchronise the stream and return the kernel status (RA_OK, RA_ERR_TIMEOUT or
+    RA_ERR_INDEX)."""
     return load().ra_sync_status(_stream(stream))
 
 
