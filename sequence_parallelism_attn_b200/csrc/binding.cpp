@@ -7,7 +7,8 @@
 // step's forward and backward 130 us (90 of them for handing a Python backward to
 // autograd's thread), against 3 and 26 us on the GPU.  The computation is the library's;
 // nothing here launches a kernel of torch's, but for a copy where an incoming gradient is
-// not dense.
+// not dense and the zeros of a backward without queries.  A call without a single token or query
+// returns empty results; the C ABI takes sizes from one up.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -87,7 +88,7 @@ void* stream_of(const Tensor& t) {
     return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
 }
 
-// Elements between tokens; the dense value where there is a single one.
+// Elements between tokens; the dense value where there is one at most.
 int64_t token_stride(const Tensor& t, int64_t dim) {
     return t.size(dim) > 1 ? t.stride(dim) : t.size(dim + 1) * t.size(dim + 2);
 }
@@ -181,6 +182,7 @@ std::optional<Tensor> paged_kv_append(const OptTensor& q, const Tensor& k, const
             out = at::empty(q->sizes(), q->options());
         }
     }
+    if (N == 0) return out;  // a step without tokens
     check(ra_paged_kv_append(
         q ? q->const_data_ptr() : nullptr, k.const_data_ptr(), v.const_data_ptr(),
         q ? token_stride(*q, 0) : 0, token_stride(k, 0), token_stride(v, 0), b.cu, b.lens,
@@ -219,6 +221,7 @@ std::tuple<Tensor, Tensor> prefix_attn_fwd(
     const int mt = narrow(std::min(max_tokens, N), "max_tokens"), n = narrow(N, "N");
     const Tensor o = result_of(out, "out", q.sizes(), out_dtype, q);
     const Tensor l = result_of(lse, "lse", {H_q, N}, at::kFloat, q);
+    if (N == 0) return {o, l};  // a step without tokens
     const Tensor ws = workspace_of(
         workspace,
         ra_prefix_attn_workspace(b.B, n, mt, ml, plen, H_q, c.H_kv, c.D, c.page_size), q);
@@ -277,6 +280,7 @@ std::tuple<Tensor, Tensor> cross_attn_fwd(const Tensor& q, const Tensor& k, cons
     const Cross c = check_cross(q, k, v, kv_lens, scale);
     const Tensor o = result_of(out, "out", q.sizes(), out_dtype, q);
     const Tensor l = result_of(lse, "lse", {c.B, c.H_q, c.Lq}, at::kFloat, q);
+    if (q.numel() == 0) return {o, l};
     const Tensor ws = workspace_of(
         workspace, ra_cross_attn_workspace(c.B, c.Lq, c.Lk, c.H_q, c.H_kv, c.D), q);
     check(ra_cross_attn_fwd(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), c.lens,
@@ -302,6 +306,8 @@ std::tuple<Tensor, Tensor, Tensor> cross_attn_bwd(const Tensor& q, const Tensor&
     check_dense(lse, "lse", dev, {c.B, c.H_q, c.Lq}, at::kFloat);
     const ra_dtype gd = dtype_of(grad_dtype);
     const auto opt = q.options().dtype(grad_dtype);
+    if (q.numel() == 0)
+        return {at::empty(q.sizes(), opt), at::zeros(k.sizes(), opt), at::zeros(k.sizes(), opt)};
     const Tensor dq = at::empty(q.sizes(), opt), dk = at::empty(k.sizes(), opt),
                  dv = at::empty(k.sizes(), opt);
     const Tensor ws =

@@ -495,7 +495,8 @@ def paged_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     be strided, as slices of one projection are), k_pages / v_pages [n_pages, page_size,
     H_kv, D], cu_tokens int32 [B + 1], seq_lens int32 [B] (the new tokens included),
     block_tables int32 [B, max_pages], inv_freq fp32 [rot_dim / 2] (None: no rotation).
-    Returns the rotated q [N, H_q, D] (q_out, which may be q itself), or None without q."""
+    Returns the rotated q [N, H_q, D] (q_out, which may be q itself), or None without q.
+    N = 0 does nothing."""
     if stream is not None:
         with _on(stream, k):
             return paged_kv_append(q, k, v, k_pages, v_pages, cu_tokens, seq_lens, block_tables,
@@ -517,7 +518,7 @@ def prefix_attn_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     shares, then each sequence's own keys up to the token itself.  cu_tokens, seq_lens and
     block_tables as for paged_kv_append; max_tokens and max_len bound them (max_len: the
     tables' capacity by default; a closer bound splits the work better).  prefix_len = 0:
-    plain paged attention.  Rows past cu_tokens[B] are not written.  Returns
+    plain paged attention.  Rows past cu_tokens[B] are not written; N = 0 does nothing.  Returns
     (out [N, H_q, D] in out_dtype, lse [H_q, N] fp32); the workspace
     (ra_prefix_attn_workspace bytes) is allocated here when not given."""
     if stream is not None:
@@ -537,7 +538,8 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                    stream=None):
     """Attention of q [B, Lq, H_q, D] to an encoder's states k, v [B, Lk, H_kv, D] (bf16;
     tokens and batch rows may be strided, k and v alike), per batch row the first kv_lens[b]
-    of them (int32 [B]; None: all) (ra_cross_attn_fwd).  Returns (out [B, Lq, H_q, D] in
+    of them (int32 [B]; None: all) (ra_cross_attn_fwd).  B = 0 or Lq = 0 does nothing (and gives
+    zero gradients of k and v in cross_attn_bwd).  Returns (out [B, Lq, H_q, D] in
     out_dtype, lse [B, H_q, Lq] fp32)."""
     if stream is not None:
         with _on(stream, q):

@@ -160,6 +160,20 @@ def test_captured_step(ra_lib):
         ref.check_grads(g, want, str(now))
 
 
+@pytest.mark.parametrize("B,Lq", [(0, 5), (2, 0)])
+def test_no_queries(ra_lib, B, Lq):
+    """Without a query the results are empty and k's and v's gradients zero."""
+    from sequence_parallelism_attn_b200 import autograd
+    q, k, v = (torch.ones(B, n, h, 64, device=DEV).bfloat16().requires_grad_()
+               for n, h in ((Lq, 4), (7, 2), (7, 2)))
+    o = autograd.cross_attention(q, k, v)
+    assert o.shape == (B, Lq, 4, 64) and o.dtype == torch.bfloat16
+    g = torch.autograd.grad(o, (q, k, v), torch.zeros_like(o))
+    assert [x.shape for x in g] == [x.shape for x in (q, k, v)] and not any(x.any() for x in g)
+    assert ra_lib.cross_attn_fwd(q, k, v)[1].shape == (B, 4, Lq)
+    assert ra_lib.ra_sync_status() == 0
+
+
 def test_fp32_inputs_are_refused(ra_lib):
     from sequence_parallelism_attn_b200 import autograd
     x = torch.zeros(1, 2, 2, 64, device=DEV)

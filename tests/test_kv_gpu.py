@@ -142,6 +142,8 @@ RAGGED = [  # one or a few long runs of new tokens among short ones, where the r
     ([1] * 300 + [77], [1 + i % 40 for i in range(300)] + [99], 48, 2, 1, 128, 50),
     ([2, 1, 1, 33, 1], [40, 3, 1000, 40, 1], 16, 130, 1, 64, 20),
     ([1, 1, 1, 9, 1, 1, 1, 1], [2000, 3, 1500, 9, 1, 0, 4000, 700], 64, 2, 2, 64, 0),  # one tile each
+    ([0] * 30 + [1] * 8 + [4], [9, 0] * 15 + [60] * 8 + [700], 16, 8, 2, 64, 3000),  # prefix by tiles
+    ([0] * 30 + [1] * 4 + [3], [9, 0] * 15 + [60] * 4 + [700], 48, 3, 1, 128, 500),  # and by rows
 ]
 
 
@@ -550,6 +552,24 @@ def test_append_of_a_very_long_run(ra_lib):
         assert torch.equal(pool[ids[B - 1:]].view(run, 1, 64), x[7:7 + run])
         assert torch.equal(pool[ids[:B - 1], 0], x[single])
         assert not pool[ids[:B - 1], 1:].any()
+
+
+def test_step_without_tokens(ra_lib):
+    """A batch whose sequences bring no token: nothing is written, the results are empty."""
+    x = Batch([0, 0], [5, 40], 16, 2, 64, 20)
+    kp, vp, cu, lens, tables, pt = x.gpu("kp", "vp", "cu", "lens", "tables", "ptable")
+    before = kp.clone(), vp.clone()
+    q, k = (torch.empty(0, h, 64, dtype=torch.bfloat16, device=DEV) for h in (4, 2))
+    r = ra_lib.paged_kv_append(q, k, k, kp, vp, cu, lens, tables, torch.ones(32, device=DEV), 1)
+    assert r.shape == (0, 4, 64) and r.dtype == torch.bfloat16
+    assert ra_lib.paged_kv_append(None, k, k, kp, vp, cu, lens, tables, None, 1) is None
+    o, l = ra_lib.prefix_attn_fwd(r, kp, vp, cu, lens, tables, 1, prefix_table=pt, prefix_len=20)
+    assert o.shape == (0, 4, 64) and l.shape == (4, 0) and o.dtype == torch.float32
+    assert all(torch.equal(a.nan_to_num(9e9), b.nan_to_num(9e9))
+               for a, b in zip(before, (kp, vp)))
+    with pytest.raises(ValueError):  # the checks are those of any call
+        ra_lib.prefix_attn_fwd(r, kp, vp, cu.long(), lens, tables, 1)
+    assert ra_lib.ra_sync_status() == 0
 
 
 def test_append_in_place_query(ra_lib):
